@@ -23,6 +23,11 @@
  *                                          -> hylra_similarity, hylra_dp_policy,
  *                                             hylra_overlap_counts,
  *                                             hylra_similarity_from_counts
+ *   Serving caches: the same attention over a paged cache, and a selection of
+ *        pages that needs no full layer.
+ *                                          -> hylra_paged_tables, hylra_paged_append,
+ *                                             hylra_paged_decode, hylra_paged_select,
+ *                                             hylra_paged_decode_topk
  *   §4   The Jump3 baseline (a reset every third layer).
  *                                          -> hylra_static_policy
  *
@@ -80,7 +85,8 @@ typedef enum {
   HYLRA_ERR_WORKSPACE = -4     /* workspace smaller than hylra_workspace_bytes */
 } hylra_error_t;
 
-typedef enum { HYLRA_BF16 = 0, HYLRA_FP32 = 1 } hylra_dtype_t;
+/* HYLRA_FP16 is a type of the paged calls only. */
+typedef enum { HYLRA_BF16 = 0, HYLRA_FP32 = 1, HYLRA_FP16 = 2 } hylra_dtype_t;
 
 /* Bits of the device status word (hylra_read_status). */
 #define HYLRA_STATUS_BAD_SEQLEN 0x1u   /* n_b < 0, > max_seqlen, or beyond the cache: sequence skipped */
@@ -88,6 +94,7 @@ typedef enum { HYLRA_BF16 = 0, HYLRA_FP32 = 1 } hylra_dtype_t;
 #define HYLRA_STATUS_DUP_INDEX 0x4u    /* a block index appears twice in one reuse list               */
 #define HYLRA_STATUS_NONFINITE 0x8u    /* a non-finite block score was met (treated as 0)             */
 #define HYLRA_STATUS_TIMEOUT 0x10u     /* a bounded wait inside a kernel gave up                      */
+#define HYLRA_STATUS_NO_PAGES 0x20u    /* paged tables: the free list ran out, a request was refused   */
 
 typedef struct hylra_shape {
   int32_t batch;         /* B, 1..HYLRA_MAX_BATCH                                        */
@@ -309,6 +316,151 @@ int hylra_static_policy(int32_t num_layers, int32_t period, uint8_t* policy,
 int hylra_decode_full_noalloc(const hylra_shape_t* shape, const void* q, const void* K,
                               const void* V, const int32_t* seqlens, float* out,
                               int32_t* topk_out, uint32_t* status_out, hylra_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache.  A serving loop keeps the K/V rows of many sequences in one
+ * pool of pages and gives each sequence a row of a block table that names its
+ * pages.  One step runs, in this order,
+ *   hylra_paged_tables   pages, slots and lengths of the step's new tokens
+ *   hylra_paged_append   the new K/V rows into their slots, and the mean key of
+ *                        every page that becomes full
+ *   hylra_paged_decode   attention of one query token over all of its sequence,
+ *                        or hylra_paged_select (the pages whose mean keys
+ *                        promise most attention mass) and
+ *                        hylra_paged_decode_topk (attention over those alone)
+ * A page plays the part that a 128-token block (HyLRA summary 2.4) plays in the
+ * calls above; hylra_paged_select replaces the full layer that a reset layer
+ * needs for its indices.
+ *
+ * Further to the conventions at the top:
+ *  * K_pages, V_pages: one pool each, element (page, head, row, i) at
+ *    page * page_stride + head * head_stride + row * token_stride + i, so a
+ *    pool may be [page][head][row][d], [page][row][head][d] or a slice of a
+ *    larger array.  Both pools have the same strides.
+ *  * block_table: int32 [B][max_pages]; entry j of row b is the page that holds
+ *    tokens j*page_size .. (j+1)*page_size - 1 of sequence b.  Entries past a
+ *    sequence's last page are not read.  A page id outside [0, num_pages) sets
+ *    HYLRA_STATUS_BAD_INDEX and its tokens are left out.
+ *  * seqlens: int32 [B], 0 .. max_pages * page_size; any other value sets
+ *    HYLRA_STATUS_BAD_SEQLEN and counts as 0.  Rows of a page past its
+ *    sequence's end may hold anything (NaN included).
+ *  * A slot is page * page_size + row.
+ *  * Two sequences may share pages that neither writes.
+ *  * Every device pointer below must belong to the current device; K/V pools,
+ *    q, out and key_means must be 16-byte aligned, int32 arrays 4-byte, the
+ *    workspace 256-byte.
+ *  * The calls are launched as programmatic dependents: their start-up overlaps
+ *    the end of the preceding kernel in the stream, and they read and write
+ *    nothing before it has completed.  All are capturable in a CUDA graph. */
+typedef struct hylra_paged {
+  int32_t batch;        /* B, 1..HYLRA_MAX_BATCH                                       */
+  int32_t num_q_heads;  /* Hq; Hq % Hkv == 0 and Hq / Hkv <= HYLRA_MAX_GROUP           */
+  int32_t num_kv_heads; /* Hkv                                                         */
+  int32_t head_dim;     /* d: 64 or 128                                                */
+  int32_t page_size;    /* tokens per page: 16, 32, 64 or 128                          */
+  int32_t dtype;        /* HYLRA_BF16 or HYLRA_FP16: q, K, V and key_means             */
+  int32_t num_pages;    /* pages of the pool; num_pages * page_size < 2^31             */
+  int32_t max_pages;    /* columns of block_table; max_pages * page_size <=
+                           HYLRA_MAX_SEQLEN                                            */
+  int64_t page_stride;  /* strides in elements: multiples of 8, below 2^39;            */
+  int64_t head_stride;  /*   rows of d elements must not overlap                       */
+  int64_t token_stride;
+  float softmax_scale;  /* logit scale; 0: 1/sqrt(d).  Finite, >= 0                    */
+} hylra_paged_t;
+
+/* Bytes of workspace the paged calls need on the current device.  One size
+ * serves every shape (it depends on the device's SM count).  Zero it once with
+ * hylra_workspace_init; every call leaves it ready for the next.  Like the
+ * other workspaces it serves one stream at a time.  Host only. */
+int hylra_paged_workspace_bytes(const hylra_paged_t* shape, size_t* bytes);
+
+/* Pages and slots for a step's new tokens.  cached_lens, new_lens: device
+ * int32 [B], tokens of request b that are in the cache and that this step
+ * adds (0 allowed).  free_pages: device int32 [free_capacity], of which the
+ * first *free_count (device int32) entries are free pages.
+ * Request b occupies have_b = ceil(cached_b / page_size) pages and needs
+ * need_b = ceil((cached_b + new_b) / page_size) - have_b more.  They come off
+ * the end of the free list, request after request, page after page, and are
+ * written to block_table[b][have_b ..]; no other entry is written.  A request
+ * that needs pages is refused, with HYLRA_STATUS_NO_PAGES, when the needs up
+ * to and with its own pass *free_count (all later ones that need pages are
+ * refused with it); one that needs none is served.
+ * Outputs: cu_new int32 [B + 1], the running sum of new_lens (refused requests
+ * keep their places); slot_map int32 [slot_capacity], the slot of each new
+ * token, request after request, -1 for a refused request's tokens and past the
+ * last one; seqlens_out int32 [B], cached + new (cached where refused; may be
+ * cached_lens itself); free_count_out int32 [1], what is left of the free list
+ * (may be free_count itself).
+ * Lengths that no table row can hold (negative, or cached + new above
+ * max_pages * page_size) and requests whose tokens do not all fit in
+ * slot_capacity are refused with HYLRA_STATUS_BAD_SEQLEN (a negative new_b
+ * counts as 0 in cu_new).  A *free_count outside 0..free_capacity counts as 0
+ * and, like a listed page or a table entry outside the pool, sets
+ * HYLRA_STATUS_BAD_INDEX; the tokens of such a page get slot -1.
+ * The pool's layout and heads are not used. */
+int hylra_paged_tables(const hylra_paged_t* shape, const int32_t* cached_lens,
+                       const int32_t* new_lens, const int32_t* free_pages,
+                       int32_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                       int32_t* seqlens_out, int32_t* cu_new, int32_t* slot_map,
+                       int32_t slot_capacity, int32_t* free_count_out, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream);
+
+/* Writes num_tokens new rows to the pools.  K_new, V_new: element (t, h, i) at
+ * t * new_stride + h * d + i (new_stride in elements, a multiple of 8 and
+ * >= Hkv * d, so a slice of a fused projection's rows will do; num_tokens may
+ * be 0).  slot_map: int32 [num_tokens]; -1 leaves a token out, any other value
+ * outside the pool does so with HYLRA_STATUS_BAD_INDEX.  A sequence's tokens
+ * must be in order and next to each other, and no slot may be named twice
+ * (hylra_paged_tables gives such maps).
+ * key_means ([num_pages][Hkv][d], may be NULL): a token that lands in the last
+ * row of its page makes the page full, and its mean key over all page_size
+ * rows (earlier rows from this call or from the pool) is written there: summed
+ * in fp32, rounded once.  The means of other pages are left as they are. */
+int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void* V_new,
+                       int64_t new_stride, const int32_t* slot_map, int32_t num_tokens,
+                       void* K_pages, void* V_pages, void* key_means, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream);
+
+/* Attention of one query token per sequence over all of its cached tokens.
+ * q: [B][Hq][d]; out: fp32 [B][Hq][d]; lse: fp32 [B][Hq] or NULL, the natural
+ * logarithm of the softmax denominator (sum of exp of the scaled logits), with
+ * which outputs over disjoint parts of a sequence can be joined.  A sequence
+ * without tokens gets zeros and -inf. */
+int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,
+                       const void* V_pages, const int32_t* block_table, const int32_t* seqlens,
+                       float* out, float* lse, void* workspace, size_t workspace_bytes,
+                       hylra_stream_t stream);
+
+/* The pages of each (sequence, KV head) that its query promises to attend to
+ * most, from the pages' mean keys alone.  NB_b = ceil(n_b / page_size).  The
+ * first `sink` and the last `recent` pages are always taken (sink >= 0,
+ * recent >= 1, so that the page still being filled, which has no mean, is
+ * among them); the others are ranked by
+ *   score_j = sum over the r q-heads g of  softmax_j(scale * q_g . mean_j),
+ * the softmax over the ranked pages: the attention mass of page j (the score of
+ * hylra_decode_full) with each key replaced by its page's mean.  Computed in 64
+ * bits and rounded once to fp32; lower page first among equal scores.
+ * page_idx: int32 [B][Hkv][topk] (1..HYLRA_MAX_TOPK): the always-taken pages in
+ * order, then the others in rank order, -1 past the last.  When topk is below
+ * the number of always-taken pages, the first topk of them.  A non-finite score
+ * counts as 0 with HYLRA_STATUS_NONFINITE; the score of a page outside the pool
+ * is 0.  B * Hkv <= 65535. */
+int hylra_paged_select(const hylra_paged_t* shape, const void* q, const void* key_means,
+                       const int32_t* block_table, const int32_t* seqlens, int32_t topk,
+                       int32_t sink, int32_t recent, int32_t* page_idx, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream);
+
+/* hylra_paged_decode restricted to the pages listed in page_idx (int32
+ * [B][Hkv][topk], per KV head, as written by hylra_paged_select or by any other
+ * rule; topk 1..HYLRA_MAX_TOPK): the softmax runs over the listed pages'
+ * tokens.  Only the first min(topk, NB_b) entries are read; -1 is skipped, any
+ * other entry outside [0, NB_b) is skipped with HYLRA_STATUS_BAD_INDEX, and a
+ * page listed twice counts twice.  An empty selection gives zeros and -inf. */
+int hylra_paged_decode_topk(const hylra_paged_t* shape, const void* q, const void* K_pages,
+                            const void* V_pages, const int32_t* block_table,
+                            const int32_t* seqlens, const int32_t* page_idx, int32_t topk,
+                            float* out, float* lse, void* workspace, size_t workspace_bytes,
+                            hylra_stream_t stream);
 
 /* Failure detection.  Every wait inside the kernels (for a TMA copy, a
  * pipeline stage, a peer CTA's data) gives up after a limit of SM clocks,

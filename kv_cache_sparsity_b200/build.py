@@ -22,8 +22,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libhylra.so")
 
-SOURCES = [os.path.join(CSRC, "hylra_api.cu"), os.path.join(CSRC, "hylra_policy.cpp")]
+SOURCES = [os.path.join(CSRC, "hylra_api.cu"), os.path.join(CSRC, "hylra_paged.cu"),
+           os.path.join(CSRC, "hylra_policy.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, "hylra_kernels.cuh"), os.path.join(CSRC, "hylra_device.cuh"),
+                  os.path.join(CSRC, "hylra_paged.cuh"), os.path.join(CSRC, "hylra_host.h"),
                   os.path.join(INCLUDE, "hylra.h")]
 GENCODE = "arch=compute_100a,code=sm_100a"
 

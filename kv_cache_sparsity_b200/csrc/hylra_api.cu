@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "hylra.h"
+#include "hylra_host.h"
 #include "hylra_kernels.cuh"
 
 using namespace hylra;
@@ -769,6 +770,14 @@ int offload_layer(void* ctx, int l, int reset_layer, int* prev_ctas) {
 }
 
 }  // namespace
+
+namespace hylra {
+
+long long host_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+
+}  // namespace hylra
 
 extern "C" {
 

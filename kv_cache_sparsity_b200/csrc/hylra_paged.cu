@@ -1,0 +1,415 @@
+// hylra_paged.cu - C ABI entry points of the paged-cache calls (see include/hylra.h).
+//
+// Host side only: argument validation, TMA descriptor encoding and launches.
+// The kernels live in hylra_paged.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+
+#include "hylra.h"
+#include "hylra_host.h"
+#include "hylra_paged.cuh"
+
+using namespace hylra;
+using namespace hylra::paged;
+
+namespace {
+
+constexpr size_t kSmemMax = 232448;  // 227 KB of dynamic shared memory per CTA
+static_assert(sizeof(DecodeSmem<128>) + 1024 <= kSmemMax, "decode kernel shared memory");
+static_assert(sizeof(DecodeSmem<64>) + 1024 <= kSmemMax, "decode kernel shared memory");
+
+struct PagedLayout {
+  size_t tickets, partials, total;
+  int G;  // CTAs of the decode kernel
+};
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int current_device(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+    return HYLRA_ERR_CUDA;
+  return HYLRA_OK;
+}
+
+// Partial slots are sized for the larger head dimension: one workspace serves
+// every shape.
+PagedLayout make_layout(int sms) {
+  PagedLayout L{};
+  L.G = std::min(sms, MAX_GRID);
+  L.tickets = 256;
+  L.partials = L.tickets + MAX_GRID * sizeof(uint32_t);
+  L.total = L.partials + (size_t)2 * L.G * DecodeShape<128>::SLOT * sizeof(float);
+  return L;
+}
+
+int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
+
+int check_paged(const hylra_paged_t* s) {
+  if (!s) return HYLRA_ERR_INVALID;
+  if (s->batch < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1 || s->num_pages < 1 ||
+      s->max_pages < 1)
+    return HYLRA_ERR_INVALID;
+  if (s->dtype != HYLRA_BF16 && s->dtype != HYLRA_FP16)
+    return s->dtype == HYLRA_FP32 ? HYLRA_ERR_UNSUPPORTED : HYLRA_ERR_INVALID;
+  if (s->num_q_heads % s->num_kv_heads != 0) return HYLRA_ERR_INVALID;
+  if (!(s->softmax_scale >= 0.f) || !std::isfinite(s->softmax_scale)) return HYLRA_ERR_INVALID;
+  if (s->head_dim != 64 && s->head_dim != 128) return HYLRA_ERR_UNSUPPORTED;
+  if (s->page_size != 16 && s->page_size != 32 && s->page_size != 64 && s->page_size != 128)
+    return HYLRA_ERR_UNSUPPORTED;
+  if (s->num_q_heads / s->num_kv_heads > HYLRA_MAX_GROUP || s->batch > HYLRA_MAX_BATCH)
+    return HYLRA_ERR_UNSUPPORTED;
+  if ((long long)s->num_pages * s->page_size > INT_MAX) return HYLRA_ERR_UNSUPPORTED;
+  if ((long long)s->max_pages * s->page_size > HYLRA_MAX_SEQLEN) return HYLRA_ERR_UNSUPPORTED;
+  const long long units = ((long long)s->max_pages * s->page_size + UTOK - 1) / UTOK;
+  if (s->num_kv_heads > INT_MAX / HYLRA_MAX_GROUP / HYLRA_MAX_BATCH ||
+      (long long)s->batch * s->num_kv_heads * units > INT_MAX / 4)
+    return HYLRA_ERR_UNSUPPORTED;
+  return HYLRA_OK;
+}
+
+// Strides of the pool: rows of d elements at (page, head, row) must not overlap.
+int check_pool(const hylra_paged_t* s) {
+  struct Dim {
+    int64_t stride, extent;
+  } dim[3] = {{s->token_stride, s->page_size},
+              {s->head_stride, s->num_kv_heads},
+              {s->page_stride, s->num_pages}};
+  for (const Dim& x : dim) {
+    if (x.stride < 0 || x.stride % 8 != 0) return HYLRA_ERR_INVALID;
+    if (x.stride >= (int64_t(1) << 39)) return HYLRA_ERR_UNSUPPORTED;
+  }
+  std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t span = s->head_dim;  // elements covered by the dimensions so far
+  for (const Dim& x : dim) {
+    if (x.extent == 1) continue;
+    if (x.stride < span) return HYLRA_ERR_INVALID;
+    if (x.extent - 1 > ((int64_t(1) << 46) - span) / x.stride) return HYLRA_ERR_UNSUPPORTED;
+    span += x.stride * (x.extent - 1);
+  }
+  return HYLRA_OK;
+}
+
+int check_workspace(const void* ws, size_t bytes, const PagedLayout& L) {
+  if (!ws || !aligned(ws, 256)) return HYLRA_ERR_INVALID;
+  return bytes < L.total ? HYLRA_ERR_WORKSPACE : HYLRA_OK;
+}
+
+bool bad_ptr(const void* p, size_t a) { return !p || !aligned(p, a); }
+
+// One pool as {64 elements, rows, d / 64, heads, pages}: a box is one page of
+// one head, its 64-column halves one after the other, 128-byte swizzle.
+int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return HYLRA_ERR_CUDA;
+  // the stride of a dimension of extent 1 is never used, but must be valid
+  auto bytes = [&](int64_t stride, int64_t extent) {
+    return (cuuint64_t)(extent == 1 ? s->head_dim : stride) * 2;
+  };
+  const cuuint64_t dims[5] = {64, (cuuint64_t)s->page_size, (cuuint64_t)(s->head_dim / 64),
+                              (cuuint64_t)s->num_kv_heads, (cuuint64_t)s->num_pages};
+  const cuuint64_t strides[4] = {bytes(s->token_stride, s->page_size), 128,
+                                 bytes(s->head_stride, s->num_kv_heads),
+                                 bytes(s->page_stride, s->num_pages)};
+  const cuuint32_t box[5] = {64, (cuuint32_t)s->page_size, (cuuint32_t)(s->head_dim / 64), 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(
+      tm, s->dtype == HYLRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      5, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HYLRA_OK : HYLRA_ERR_CUDA;
+}
+
+// Opt a kernel in to the full shared memory, once per device.  `done` holds
+// one bit per device.
+template <typename Kernel>
+int allow_smem(Kernel kernel, std::atomic<uint64_t>& done, int dev) {
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return HYLRA_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) !=
+      cudaSuccess)
+    return HYLRA_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_release);
+  return HYLRA_OK;
+}
+
+// Launch as a programmatic dependent of the preceding kernel, in clusters of
+// `cluster` CTAs along x.
+template <typename Kernel, typename... Args>
+int launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+           const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? HYLRA_OK : HYLRA_ERR_CUDA;
+}
+
+template <int HD, typename T, bool LIST>
+int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeParams& p, int G,
+                  int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = paged_decode_kernel<HD, T, LIST>;
+  if (int rc = allow_smem(kernel, done, dev)) return rc;
+  return launch(kernel, dim3(G), NTHR, sizeof(DecodeSmem<HD>) + 1024, stream, 1, tmK, tmV, p);
+}
+
+int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
+           const int32_t* table, const int32_t* seqlens, const int32_t* list, int k, bool use_list,
+           float* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_paged(s);
+  if (rc || (rc = check_pool(s))) return rc;
+  if (bad_ptr(q, 16) || bad_ptr(K, 16) || bad_ptr(V, 16) || bad_ptr(out, 16) ||
+      bad_ptr(table, 4) || bad_ptr(seqlens, 4) || !aligned(lse, 4))
+    return HYLRA_ERR_INVALID;
+  if (use_list && (bad_ptr(list, 4) || k < 1)) return HYLRA_ERR_INVALID;
+  if (use_list && k > HYLRA_MAX_TOPK) return HYLRA_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if ((rc = current_device(&dev, &sms))) return rc;
+  const PagedLayout L = make_layout(sms);
+  if ((rc = check_workspace(ws, ws_bytes, L))) return rc;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  DecodeParams p{};
+  p.q = q;
+  p.table = table;
+  p.seqlens = seqlens;
+  p.list = list;
+  p.out = out;
+  p.lse = lse;
+  p.status = reinterpret_cast<uint32_t*>(w);
+  p.tickets = reinterpret_cast<uint32_t*>(w + L.tickets);
+  p.partials = reinterpret_cast<float*>(w + L.partials);
+  p.B = s->batch;
+  p.Hq = s->num_q_heads;
+  p.Hkv = s->num_kv_heads;
+  p.r = s->num_q_heads / s->num_kv_heads;
+  p.k = k;
+  p.ps_log2 = log2_of(s->page_size);
+  p.num_pages = s->num_pages;
+  p.max_pages = s->max_pages;
+  const double scale =
+      s->softmax_scale > 0.f ? (double)s->softmax_scale : 1.0 / std::sqrt((double)s->head_dim);
+  p.scale_log2 = (float)(1.4426950408889634 * scale);
+  p.wait_limit = host_wait_limit();
+  CUtensorMap tmK, tmV;
+  if ((rc = pool_map(&tmK, K, s)) || (rc = pool_map(&tmV, V, s))) return rc;
+  const bool bf = s->dtype == HYLRA_BF16;
+#define HYLRA_DECODE(HD, LIST)                                                              \
+  (bf ? launch_decode<HD, __nv_bfloat16, LIST>(tmK, tmV, p, L.G, dev, stream)              \
+      : launch_decode<HD, __half, LIST>(tmK, tmV, p, L.G, dev, stream))
+  if (s->head_dim == 128) return use_list ? HYLRA_DECODE(128, true) : HYLRA_DECODE(128, false);
+  return use_list ? HYLRA_DECODE(64, true) : HYLRA_DECODE(64, false);
+#undef HYLRA_DECODE
+}
+
+template <int HD, typename T>
+int launch_select(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
+                  cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = paged_select_kernel<HD, T>;
+  if (int rc = allow_smem(kernel, done, dev)) return rc;
+  return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
+}
+
+template <int HD, typename T>
+int launch_append(const AppendParams& p, int tiles, cudaStream_t stream) {
+  return launch(paged_append_kernel<HD, T>, dim3(tiles, p.Hkv), NT_APP, 0, stream, 1, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int hylra_paged_workspace_bytes(const hylra_paged_t* shape, size_t* bytes) {
+  int rc = check_paged(shape);
+  if (rc) return rc;
+  if (!bytes) return HYLRA_ERR_INVALID;
+  int dev = 0, sms = 0;
+  if ((rc = current_device(&dev, &sms))) return rc;
+  *bytes = make_layout(sms).total;
+  return HYLRA_OK;
+}
+
+int hylra_paged_tables(const hylra_paged_t* shape, const int32_t* cached_lens,
+                       const int32_t* new_lens, const int32_t* free_pages,
+                       int32_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                       int32_t* seqlens_out, int32_t* cu_new, int32_t* slot_map,
+                       int32_t slot_capacity, int32_t* free_count_out, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream) {
+  int rc = check_paged(shape);
+  if (rc) return rc;
+  if (free_capacity < 0 || slot_capacity < 0) return HYLRA_ERR_INVALID;
+  if (bad_ptr(cached_lens, 4) || bad_ptr(new_lens, 4) || bad_ptr(free_count, 4) ||
+      bad_ptr(block_table, 4) || bad_ptr(seqlens_out, 4) || bad_ptr(cu_new, 4) ||
+      bad_ptr(free_count_out, 4) || (free_capacity > 0 && bad_ptr(free_pages, 4)) ||
+      (slot_capacity > 0 && bad_ptr(slot_map, 4)))
+    return HYLRA_ERR_INVALID;
+  int dev = 0, sms = 0;
+  if ((rc = current_device(&dev, &sms))) return rc;
+  const PagedLayout L = make_layout(sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, L))) return rc;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  TablesParams p{};
+  p.cached = cached_lens;
+  p.added = new_lens;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.table = block_table;
+  p.seqlens = seqlens_out;
+  p.cu = cu_new;
+  p.slots = slot_map;
+  p.free_left = free_count_out;
+  p.status = reinterpret_cast<uint32_t*>(w);
+  p.ticket = reinterpret_cast<uint32_t*>(w + L.tickets);
+  p.B = shape->batch;
+  p.ps_log2 = log2_of(shape->page_size);
+  p.num_pages = shape->num_pages;
+  p.max_pages = shape->max_pages;
+  p.free_cap = free_capacity;
+  p.slot_cap = slot_capacity;
+  const long long per_cta = 4 * NT_TAB;
+  const int ctas = (int)std::min<long long>(
+      sms, std::max<long long>(1, (slot_capacity + per_cta - 1) / per_cta));
+  return launch(paged_tables_kernel, dim3(ctas), NT_TAB, 0, (cudaStream_t)stream, 1, p);
+}
+
+int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void* V_new,
+                       int64_t new_stride, const int32_t* slot_map, int32_t num_tokens,
+                       void* K_pages, void* V_pages, void* key_means, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream) {
+  int rc = check_paged(shape);
+  if (rc || (rc = check_pool(shape))) return rc;
+  if (num_tokens < 0 || shape->num_kv_heads > 65535)
+    return num_tokens < 0 ? HYLRA_ERR_INVALID : HYLRA_ERR_UNSUPPORTED;
+  const int64_t width = (int64_t)shape->num_kv_heads * shape->head_dim;
+  if (num_tokens > 0 &&
+      (bad_ptr(K_new, 16) || bad_ptr(V_new, 16) || bad_ptr(slot_map, 4) || new_stride < width ||
+       new_stride % 8 != 0))
+    return HYLRA_ERR_INVALID;
+  if (new_stride >= (int64_t(1) << 31)) return HYLRA_ERR_UNSUPPORTED;
+  if (bad_ptr(K_pages, 16) || bad_ptr(V_pages, 16) || !aligned(key_means, 16))
+    return HYLRA_ERR_INVALID;
+  int dev = 0, sms = 0;
+  if ((rc = current_device(&dev, &sms))) return rc;
+  const PagedLayout L = make_layout(sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, L))) return rc;
+  if (num_tokens == 0) return HYLRA_OK;
+  AppendParams p{};
+  p.K_new = static_cast<const uint16_t*>(K_new);
+  p.V_new = static_cast<const uint16_t*>(V_new);
+  p.slots = slot_map;
+  p.K = static_cast<uint16_t*>(K_pages);
+  p.V = static_cast<uint16_t*>(V_pages);
+  p.means = static_cast<uint16_t*>(key_means);
+  p.status = static_cast<uint32_t*>(workspace);
+  p.new_stride = new_stride;
+  p.page_stride = shape->page_stride;
+  p.head_stride = shape->head_stride;
+  p.token_stride = shape->token_stride;
+  p.tokens = num_tokens;
+  p.Hkv = shape->num_kv_heads;
+  p.ps_log2 = log2_of(shape->page_size);
+  p.num_slots = shape->num_pages * shape->page_size;
+  // few tokens: a CTA each, so that they spread over the SMs
+  const long long rows = (long long)num_tokens * p.Hkv;
+  p.tile = (int)std::min<long long>(TILE_APP, std::max<long long>(1, rows / (4LL * sms)));
+  const int tiles = (num_tokens + p.tile - 1) / p.tile;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (shape->head_dim == 128)
+    return shape->dtype == HYLRA_BF16 ? launch_append<128, __nv_bfloat16>(p, tiles, st)
+                                      : launch_append<128, __half>(p, tiles, st);
+  return shape->dtype == HYLRA_BF16 ? launch_append<64, __nv_bfloat16>(p, tiles, st)
+                                    : launch_append<64, __half>(p, tiles, st);
+}
+
+int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,
+                       const void* V_pages, const int32_t* block_table, const int32_t* seqlens,
+                       float* out, float* lse, void* workspace, size_t workspace_bytes,
+                       hylra_stream_t stream) {
+  return decode(shape, q, K_pages, V_pages, block_table, seqlens, nullptr, 0, false, out, lse,
+                workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+int hylra_paged_select(const hylra_paged_t* shape, const void* q, const void* key_means,
+                       const int32_t* block_table, const int32_t* seqlens, int32_t topk,
+                       int32_t sink, int32_t recent, int32_t* page_idx, void* workspace,
+                       size_t workspace_bytes, hylra_stream_t stream) {
+  int rc = check_paged(shape);
+  if (rc) return rc;
+  if (topk < 1 || sink < 0 || recent < 1) return HYLRA_ERR_INVALID;
+  if (topk > HYLRA_MAX_TOPK) return HYLRA_ERR_UNSUPPORTED;
+  const long long nbh = (long long)shape->batch * shape->num_kv_heads;
+  if (nbh > 65535) return HYLRA_ERR_UNSUPPORTED;
+  if (bad_ptr(q, 16) || bad_ptr(key_means, 16) || bad_ptr(block_table, 4) ||
+      bad_ptr(seqlens, 4) || bad_ptr(page_idx, 4))
+    return HYLRA_ERR_INVALID;
+  int dev = 0, sms = 0;
+  if ((rc = current_device(&dev, &sms))) return rc;
+  const PagedLayout L = make_layout(sms);
+  if ((rc = check_workspace(workspace, workspace_bytes, L))) return rc;
+  SelectParams p{};
+  p.q = q;
+  p.means = key_means;
+  p.table = block_table;
+  p.seqlens = seqlens;
+  p.idx = page_idx;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.B = shape->batch;
+  p.Hq = shape->num_q_heads;
+  p.Hkv = shape->num_kv_heads;
+  p.r = shape->num_q_heads / shape->num_kv_heads;
+  p.k = topk;
+  p.sink = std::min(sink, shape->max_pages);
+  p.recent = std::min(recent, shape->max_pages);
+  p.ps_log2 = log2_of(shape->page_size);
+  p.num_pages = shape->num_pages;
+  p.max_pages = shape->max_pages;
+  p.scale = shape->softmax_scale > 0.f ? (double)shape->softmax_scale
+                                       : 1.0 / std::sqrt((double)shape->head_dim);
+  // CTAs per (sequence, KV head): until they fill the SMs a few times over, or
+  // their shares of the pages fit in shared memory
+  int cs = 1;
+  auto need = [&](int c) { return select_smem(p.r, (p.max_pages + c - 1) / c, p.max_pages); };
+  while (cs < MAX_CS && (nbh * cs * 2 <= 4LL * sms || need(cs) > kSmemMax)) cs *= 2;
+  if (need(cs) > kSmemMax) return HYLRA_ERR_UNSUPPORTED;
+  p.ppc = (p.max_pages + cs - 1) / cs;
+  const size_t smem = need(cs);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (shape->head_dim == 128)
+    return shape->dtype == HYLRA_BF16
+               ? launch_select<128, __nv_bfloat16>(p, cs, smem, (int)nbh, dev, st)
+               : launch_select<128, __half>(p, cs, smem, (int)nbh, dev, st);
+  return shape->dtype == HYLRA_BF16
+             ? launch_select<64, __nv_bfloat16>(p, cs, smem, (int)nbh, dev, st)
+             : launch_select<64, __half>(p, cs, smem, (int)nbh, dev, st);
+}
+
+int hylra_paged_decode_topk(const hylra_paged_t* shape, const void* q, const void* K_pages,
+                            const void* V_pages, const int32_t* block_table,
+                            const int32_t* seqlens, const int32_t* page_idx, int32_t topk,
+                            float* out, float* lse, void* workspace, size_t workspace_bytes,
+                            hylra_stream_t stream) {
+  return decode(shape, q, K_pages, V_pages, block_table, seqlens, page_idx, topk, true, out, lse,
+                workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,1312 @@
+// hylra_paged.cuh - kernels over a paged K/V cache for sm_100a.
+//
+//   * paged_tables_kernel: pages, slots and lengths of a step's new tokens.
+//   * paged_append_kernel: K/V rows into their slots, mean keys of full pages.
+//   * paged_select_kernel: per (sequence, KV head) the pages whose mean keys
+//     promise most attention mass; one thread-block cluster each.
+//   * paged_decode_kernel: attention of one query token over all pages of its
+//     sequence or over a list of them; persistent CTAs over a static split of
+//     all (sequence, KV head, 128 tokens) units, partial results joined by the
+//     last CTA that finishes a head.
+//
+// Every kernel is launched as a programmatic dependent and waits for the
+// preceding kernel before its first access to global memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <type_traits>
+
+#include "hylra.h"
+#include "hylra_device.cuh"
+
+namespace hylra {
+namespace paged {
+
+constexpr int GRP = HYLRA_MAX_GROUP;  // q-heads per KV head, the padded MMA N
+constexpr int UTOK = 128;             // tokens per unit of work
+constexpr int MAX_GRID = 256;         // CTAs of the decode kernel
+constexpr int MAX_B = HYLRA_MAX_BATCH;
+
+// ------------------------------------------------------------ element types
+
+template <typename T>
+struct Elem;
+
+// P is multiplied with V on the 16-bit matrix units.  Rounding P to one 16-bit
+// value would cost 2^-9 (bf16) of every weight in a result that is kept in
+// fp32, so P goes in as a sum of 16-bit terms: three bf16 terms hold all 24
+// bits of an fp32 value, two fp16 terms 22 bits.  fp16 has few exponents: P is
+// scaled by 2^12 there (P <= 1, so the first term stays below 65504), which
+// keeps the second term's rounding below 2^-36 of the largest weight.  The
+// scale cancels in O / Z.
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int SPLIT = 3;
+  static constexpr float SHIFT = 0.f, SCALE = 1.f;
+  static __device__ __forceinline__ uint16_t bits(float x) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  }
+  static __device__ __forceinline__ float value(uint16_t b) {
+    return __uint_as_float((uint32_t)b << 16);
+  }
+  static __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0,
+                                             uint32_t b1) {
+    mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+  }
+};
+
+template <>
+struct Elem<__half> {
+  static constexpr int SPLIT = 2;
+  static constexpr float SHIFT = 12.f, SCALE = 4096.f;
+  static __device__ __forceinline__ uint16_t bits(float x) {
+    return __half_as_ushort(__float2half_rn(x));
+  }
+  static __device__ __forceinline__ float value(uint16_t b) {
+    return __half2float(__ushort_as_half(b));
+  }
+  static __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0,
+                                             uint32_t b1) {
+    mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+  }
+};
+
+// ----------------------------------------------------------------- decode
+
+constexpr int NWC = 8;                   // consumer warps
+constexpr int NTC = NWC * 32;            // consumer threads
+constexpr int NTHR = NTC + 32;           // and one producer warp
+constexpr int BAR_ID = 1;                // named barrier of the consumers
+constexpr int PPITCH = UTOK + 8;         // 16-bit words per row of P: rows 4 banks apart
+constexpr int MAX_UPAGES = UTOK / 16;    // pages per unit at the smallest page
+
+struct DecodeParams {
+  const void* q;
+  const int32_t* table;
+  const int32_t* seqlens;
+  const int32_t* list;  // page list (LIST kernels)
+  float* out;
+  float* lse;           // may be null
+  uint32_t* status;
+  uint32_t* tickets;    // [MAX_GRID]
+  float* partials;      // [2 * gridDim.x][slot_floats]
+  int B, Hq, Hkv, r, k;
+  int ps_log2;          // page size
+  int num_pages, max_pages;
+  float scale_log2;     // softmax scale * log2(e)
+  long long wait_limit;
+};
+
+template <int HD>
+struct DecodeShape {
+  static constexpr int STAGE = 2 * UTOK * HD * 2;          // K and V of one unit
+  static constexpr int NST = HD == 128 ? 3 : 6;            // ring stages (192 KB)
+  static constexpr int NDG = HD / 16;                      // 16-dim groups of O
+  static constexpr int NTH = NWC / NDG;                    // token halves per dim group
+  static constexpr int SLOT = GRP * HD + 2 * GRP;          // partial: O, m, Z
+};
+
+template <int HD>
+struct DecodeSmem {
+  using S = DecodeShape<HD>;
+  uint8_t stage[S::NST][S::STAGE];  // 1024-byte aligned (128-byte swizzle atoms)
+  uint8_t qslot[S::NST][GRP * HD * 2];
+  uint16_t P[2][3][GRP][PPITCH];    // split weights of the unit's tokens, two buffers
+  float mref[2][GRP][NWC];          // what each warp's weights are relative to
+  float zs[NWC][GRP];
+  float oh[S::NTH > 1 ? GRP * HD : 4];  // second token half's O at a segment end
+  int nv[S::NST][MAX_UPAGES];       // valid rows of each page of the unit
+  alignas(8) uint64_t fullK[S::NST];
+  alignas(8) uint64_t fullV[S::NST];
+  alignas(8) uint64_t empty[S::NST];
+  int prefix[MAX_B + 1];            // units before sequence b (all heads)
+  int lens[MAX_B];
+  int abort;
+  int last[2];
+};
+
+struct Unit {
+  int b, h, j, U;  // part j of the U units of (b, h)
+};
+
+__device__ __forceinline__ Unit locate(const int* prefix, int B, int Hkv, int u) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  Unit x;
+  x.b = lo;
+  x.U = (prefix[lo + 1] - prefix[lo]) / Hkv;
+  const int off = u - prefix[lo];
+  x.h = off / x.U;
+  x.j = off - x.h * x.U;
+  return x;
+}
+
+__device__ __forceinline__ void advance(const int* prefix, int B, int Hkv, Unit& x) {
+  if (++x.j < x.U) return;
+  x.j = 0;
+  if (++x.h < Hkv) return;
+  x.h = 0;
+  do { ++x.b; } while (x.b < B && prefix[x.b + 1] == prefix[x.b]);
+  if (x.b < B) x.U = (prefix[x.b + 1] - prefix[x.b]) / Hkv;
+}
+
+// CTA that holds unit u when CTA c holds [floor(c*T/G), floor((c+1)*T/G)), G <= T.
+__device__ __forceinline__ int unit_owner(long long u, long long T, int G) {
+  return (int)(((u + 1) * G - 1) / T);
+}
+
+// Length of sequence b; a length that no table row can hold counts as 0.
+__device__ __forceinline__ int checked_len(const int32_t* seqlens, int b, int cap,
+                                           uint32_t* status, bool report) {
+  const int n = __ldcg(seqlens + b);
+  if (n >= 0 && n <= cap) return n;
+  if (report) atomicOr(status, HYLRA_STATUS_BAD_SEQLEN);
+  return 0;
+}
+
+// O, m and Z of the contributors of one head joined by log-sum-exp, by the
+// consumer threads of the CTA that finished last.
+template <int HD>
+__device__ void join_partials(const DecodeParams& p, DecodeSmem<HD>& sm, int b, int h, int first,
+                              int nc, float shift, int ct) {
+  using S = DecodeShape<HD>;
+  float* w = reinterpret_cast<float*>(&sm.P[0][0][0][0]);           // [nc][GRP] weights
+  float4* red = reinterpret_cast<float4*>(w + MAX_GRID * GRP);      // [NTC]
+  static_assert(sizeof(sm.P) >= (MAX_GRID * GRP + NTC * 4) * sizeof(float), "join scratch");
+  const int cw = ct >> 5, lane = ct & 31, r = p.r;
+  // contributor c of the head: its first unit's CTA left slot 2c + 1, the others slot 2c
+  auto slot = [&](int c) {
+    return p.partials + (size_t)(2 * (first + c) + (c == 0 ? 1 : 0)) * S::SLOT;
+  };
+  if (cw < r) {  // warp g: weights of head g
+    float m = -INFINITY;
+    for (int c = lane; c < nc; c += 32) m = fmaxf(m, __ldcg(slot(c) + GRP * HD + cw));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float z = 0.f;
+    for (int c = lane; c < nc; c += 32) {
+      const float f =
+          m == -INFINITY ? 0.f : ex2_approx(__ldcg(slot(c) + GRP * HD + cw) - m);
+      w[c * GRP + cw] = f;
+      z += f * __ldcg(slot(c) + GRP * HD + GRP + cw);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    if (lane == 0) {
+      sm.zs[0][cw] = z;
+      if (p.lse)
+        p.lse[(size_t)b * p.Hq + (size_t)h * r + cw] =
+            z == 0.f ? -INFINITY : (m + (log2f(z) - shift)) * 0.69314718f;
+    }
+  }
+  named_bar_sync(BAR_ID, NTC);
+  const int ncol = r * (HD / 4);
+  const int groups = NTC / ncol;  // >= 1: ncol <= 256
+  const int q = ct / ncol, col = ct - q * ncol;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (q < groups) {
+    const int g = col / (HD / 4), d4 = col % (HD / 4);
+#pragma unroll 4
+    for (int c = q; c < nc; c += groups) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c) + g * HD + 4 * d4));
+      const float f = w[c * GRP + g];
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+  }
+  red[ct] = acc;
+  named_bar_sync(BAR_ID, NTC);
+  if (q == 0) {
+    const int g = col / (HD / 4), d4 = col % (HD / 4);
+    for (int o = 1; o < groups; ++o) {
+      const float4 v = red[o * ncol + col];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float z = sm.zs[0][g], rz = z == 0.f ? 0.f : 1.f / z;
+    float4* dst = reinterpret_cast<float4*>(
+        p.out + ((size_t)b * p.Hq + (size_t)h * r + g) * HD + 4 * d4);
+    *dst = make_float4(acc.x * rz, acc.y * rz, acc.z * rz, acc.w * rz);
+  }
+  named_bar_sync(BAR_ID, NTC);  // the scratch may be used again
+}
+
+template <int HD, typename T, bool LIST>
+__global__ void __launch_bounds__(NTHR, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ DecodeParams p) {
+  using S = DecodeShape<HD>;
+  using E = Elem<T>;
+  constexpr int NST = S::NST;
+  extern __shared__ uint8_t smem_raw[];
+  DecodeSmem<HD>& sm = *reinterpret_cast<DecodeSmem<HD>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.fullK[s], 1);
+      mbar_init(&sm.fullV[s], 1);
+      mbar_init(&sm.empty[s], NWC);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == 32) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  for (int i = tid; i < NST * MAX_UPAGES; i += NTHR) (&sm.nv[0][0])[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // units of each sequence, then their running sum
+  const int psl = p.ps_log2, ps = 1 << psl;
+  for (int b = tid; b < p.B; b += NTHR) {
+    const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, blockIdx.x == 0);
+    const int nb = (n + ps - 1) >> psl;
+    const int tokens = LIST ? min(p.k, nb) << psl : n;
+    sm.lens[b] = n;
+    sm.prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (p.B + 31) / 32;
+    const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += sm.prefix[b + 1];
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    int run = incl - sum;
+    for (int b = b0; b < b1; ++b) {
+      run += sm.prefix[b + 1];
+      sm.prefix[b + 1] = run;
+    }
+    if (lane == 0) sm.prefix[0] = 0;
+  }
+  __syncthreads();
+  const int total = sm.prefix[p.B];
+  const int G = total > 0 ? min((int)gridDim.x, total) : 1;
+  const bool works = (int)blockIdx.x < G && total > 0;
+  const int lo = works ? (int)((long long)blockIdx.x * total / G) : 0;
+  const int hi = works ? (int)((long long)(blockIdx.x + 1) * total / G) : 0;
+  const int n = hi - lo;
+  volatile int* abort_flag = &sm.abort;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    if (n == 0) return;
+    const uint64_t pol = l2_evict_first_policy();
+    const int ppl = 7 - psl, ppu = 1 << ppl;  // pages per unit
+    const int UB = 32 >> ppl;                 // units whose pages one warp-wide fetch covers
+    const uint32_t page_bytes = (uint32_t)(ps * HD * 2);
+    const uint32_t qbytes = (uint32_t)(p.r * HD * 2);
+    const uint8_t* qbase = static_cast<const uint8_t*>(p.q);
+    // lane l: page l % ppu of unit base + l / ppu
+    int f_page, f_rows, f_b, f_h, f_start;
+    auto fetch = [&](int base) {
+      f_page = f_rows = f_b = f_h = f_start = 0;
+      const int ui = base + (lane >> ppl);
+      if (ui >= n) return;
+      const Unit x = locate(sm.prefix, p.B, p.Hkv, lo + ui);
+      f_b = x.b;
+      f_h = x.h;
+      f_start = ui == 0 || x.j == 0;
+      const int len = sm.lens[x.b], nb = (len + ps - 1) >> psl;
+      const int e = (x.j << ppl) + (lane & (ppu - 1));
+      if (e >= (LIST ? min(p.k, nb) : nb)) return;
+      int j = e;
+      if (LIST) {
+        j = __ldcg(p.list + ((size_t)x.b * p.Hkv + x.h) * p.k + e);
+        if (j < 0 || j >= nb) {
+          if (j != -1) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+          return;
+        }
+      }
+      const int pg = __ldcg(p.table + (size_t)x.b * p.max_pages + j);
+      if (pg < 0 || pg >= p.num_pages) {
+        atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+        return;
+      }
+      f_page = pg;
+      f_rows = min(ps, len - (j << psl));
+    };
+    fetch(0);
+    int issued = 0;  // units 0 .. issued-1 have started their stage's phase
+    bool ok = true;
+    for (int base = 0; base < n && ok; base += UB) {
+      const int page = f_page, rows = f_rows, ub = f_b, uh = f_h, ust = f_start;
+      const int cnt = min(UB, n - base);
+      for (int k = 0; k < cnt; ++k) {
+        const int i = base + k, s = i % NST;
+        const uint32_t ph = (uint32_t)((i / NST) & 1);
+        // after a failed wait nothing more is issued: the consumers no longer
+        // wait for stages, so a refill could land in a stage still being read
+        ok = mbar_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, p.wait_limit);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        const int src = (k << ppl) + (lane & (ppu - 1));
+        const int pg = __shfl_sync(0xffffffffu, page, src);
+        const int rw = __shfl_sync(0xffffffffu, rows, src);
+        const int b = __shfl_sync(0xffffffffu, ub, k << ppl);
+        const int h = __shfl_sync(0xffffffffu, uh, k << ppl);
+        const int start = __shfl_sync(0xffffffffu, ust, k << ppl);
+        const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rw > 0));
+        if (lane < MAX_UPAGES) sm.nv[s][lane] = lane < ppu ? rw : 0;
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bytes = np * page_bytes, bytesK = bytes + (start ? qbytes : 0u);
+          if (bytesK) mbar_arrive_expect_tx(&sm.fullK[s], bytesK); else mbar_arrive(&sm.fullK[s]);
+          if (bytes) mbar_arrive_expect_tx(&sm.fullV[s], bytes); else mbar_arrive(&sm.fullV[s]);
+          if (start)
+            bulk_load(sm.qslot[s], qbase + ((size_t)b * p.Hq + (size_t)h * p.r) * HD * 2, qbytes,
+                      &sm.fullK[s]);
+        }
+        __syncwarp();
+        const int at = lane & 15;  // lanes 0..15 the K pages, 16..31 the V pages
+        if (at < ppu && rw > 0) {
+          uint8_t* dst = sm.stage[s] + (lane < 16 ? 0 : S::STAGE / 2) + (size_t)at * page_bytes;
+          tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, 0, 0, h, pg,
+                      lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
+        }
+        issued = i + 1;
+        if (k == 0) fetch(base + UB);  // while the ring is full
+      }
+    }
+    // never exit with a copy into this CTA's shared memory in flight
+    for (int t = 0; t < NST && t < issued; ++t) {
+      const int lastu = t + (issued - 1 - t) / NST * NST;  // last unit of stage t
+      const uint32_t ph = (uint32_t)((lastu / NST) & 1);
+      if (!mbar_drain(&sm.fullK[t], ph) || !mbar_drain(&sm.fullV[t], ph)) *abort_flag = 1;
+    }
+    if (*abort_flag && lane == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  const int cw = warp - 1, ct = tid - 32;
+  const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
+  const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
+  // sequences without units: zeros and -inf
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (sm.prefix[b + 1] != sm.prefix[b]) continue;
+    for (int i = ct; i < p.Hq * HD; i += NTC) p.out[(size_t)b * p.Hq * HD + i] = 0.f;
+    if (p.lse)
+      for (int i = ct; i < p.Hq; i += NTC) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+  }
+  if (n == 0) return;
+
+  const uint32_t half_bytes = (uint32_t)ps * 128u, page_bytes = (uint32_t)ps * HD * 2u;
+  auto tok_base = [&](int t) {  // offset of token t's row (t a multiple of 16) in K or V
+    return (uint32_t)(t >> psl) * page_bytes + (uint32_t)(t & (ps - 1)) * 128u;
+  };
+  const uint32_t kofs = tok_base(cw * 16) + (uint32_t)(xr + (mi & 1) * 8) * 128u;
+  const int kchi = mi >> 1;
+  // V: this warp's 16 dims of O, all tokens or every second half of them
+  const int dg = cw % S::NDG, th = cw / S::NDG;
+  constexpr int CPW = 8 / S::NTH;  // 16-token chunks per warp
+  const int vch = 2 * dg + (mi & 1);
+  const uint32_t vsub = (uint32_t)(vch >> 3) * half_bytes + (uint32_t)(((vch & 7) ^ xr) << 4) +
+                        (uint32_t)(xr + (mi >> 1) * 8) * 128u;
+  const float sl = p.scale_log2;
+
+  uint32_t qf[HD / 16][2];
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  float m_run[2] = {-INFINITY, -INFINITY}, z_run[2] = {0.f, 0.f};
+  Unit x = locate(sm.prefix, p.B, p.Hkv, lo);
+  int npend = 0;
+  int pend_b[2], pend_h[2], pend_first[2], pend_nc[2];
+  bool seg_has_start = false;
+
+  for (int i = 0; i < n; ++i) {
+    const int s = i % NST, buf = i & 1;
+    const uint32_t ph = (uint32_t)((i / NST) & 1);
+    const bool seg_start = i == 0 || x.j == 0;
+    const bool seg_end = i == n - 1 || x.j == x.U - 1;
+    mbar_wait_bounded(&sm.fullK[s], ph, abort_flag, p.wait_limit);
+    const int nvw = min(16, max(0, sm.nv[s][(cw * 16) >> psl] - ((cw * 16) & (ps - 1))));
+    if (seg_start) {
+      seg_has_start = x.j == 0;
+      const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.qslot[s]);
+#pragma unroll
+      for (int kt = 0; kt < HD / 16; ++kt) {
+        qf[kt][0] = g4 < p.r ? qs[(g4 * HD + kt * 16 + 2 * c4) >> 1] : 0u;
+        qf[kt][1] = g4 < p.r ? qs[(g4 * HD + kt * 16 + 8 + 2 * c4) >> 1] : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = 0.f;
+      m_run[0] = m_run[1] = -INFINITY;
+      z_run[0] = z_run[1] = 0.f;
+    }
+    // S^T = K Q^T for this warp's 16 tokens (raw logits; e & 2: token g4 + 8)
+    float a[4];
+    {
+      float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t kb = smem_u32(sm.stage[s]) + kofs;
+#pragma unroll
+      for (int kt = 0; kt < HD / 16; ++kt) {
+        const int ch = 2 * kt + kchi;
+        uint32_t f[4];
+        ldsm_x4(kb + (uint32_t)(ch >> 3) * half_bytes + (uint32_t)(((ch & 7) ^ xr) << 4), f[0],
+                f[1], f[2], f[3]);
+        E::mma((kt & 1) ? a1 : a0, f, qf[kt][0], qf[kt][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        a[e] = g4 + ((e & 2) ? 8 : 0) < nvw ? a0[e] + a1[e] : -INFINITY;
+    }
+    // largest logit of the warp's tokens per head; the weights are taken
+    // relative to the running maximum or to it, whichever is larger, so that
+    // they are ready before the other warps' maxima are known
+    float mx[2] = {fmaxf(a[0], a[2]), fmaxf(a[1], a[3])};
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+    }
+    float ref[2], sub[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ref[e] = fmaxf(m_run[e], mx[e] * sl);
+      sub[e] = ref[e] == -INFINITY ? 0.f : ref[e];
+    }
+    float w[4], sum[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = ex2_approx(fmaf(a[e], sl, -sub[e & 1])) * E::SCALE;
+    sum[0] = w[0] + w[2];
+    sum[1] = w[1] + w[3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int head = (e & 1) ? h1 : h0, tok = cw * 16 + g4 + ((e & 2) ? 8 : 0);
+      float rest = w[e];
+#pragma unroll
+      for (int t = 0; t < E::SPLIT; ++t) {
+        const uint16_t hb = E::bits(rest);
+        sm.P[buf][t][head][tok] = hb;
+        rest -= E::value(hb);
+      }
+    }
+    if (g4 == 0) {
+      sm.mref[buf][h0][cw] = ref[0];
+      sm.mref[buf][h1][cw] = ref[1];
+    }
+    mbar_wait_bounded(&sm.fullV[s], ph, abort_flag, p.wait_limit);
+    if (nvw < 16) {
+      // rows past the end, or of pages that were not loaded, may hold anything
+      // (NaN included): zero weights need zero values
+      uint8_t* vrow = sm.stage[s] + S::STAGE / 2 + tok_base(cw * 16);
+      constexpr int CH = HD / 8;  // 16-byte chunks per row
+      for (int idx = lane; idx < 16 * CH; idx += 32) {
+        const int row = idx / CH, ch = idx % CH;
+        if (row >= nvw)
+          *reinterpret_cast<uint4*>(vrow + (ch >> 3) * half_bytes + row * 128 + (ch & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    }
+    named_bar_sync(BAR_ID, NTC);  // P, mref and the zeroed rows of all warps
+    float m_new[2], rw[2][NWC];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4* src = reinterpret_cast<const float4*>(sm.mref[buf][e ? h1 : h0]);
+      const float4 u = src[0], v = src[1];
+      rw[e][0] = u.x; rw[e][1] = u.y; rw[e][2] = u.z; rw[e][3] = u.w;
+      rw[e][4] = v.x; rw[e][5] = v.y; rw[e][6] = v.z; rw[e][7] = v.w;
+      m_new[e] = m_run[e];
+#pragma unroll
+      for (int t = 0; t < NWC; ++t) m_new[e] = fmaxf(m_new[e], rw[e][t]);
+    }
+    const bool moved =
+        __any_sync(0xffffffffu, m_new[0] != m_run[0] || m_new[1] != m_run[1]);
+    if (moved) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // -inf - -inf only where nothing was attended to yet: all terms are 0
+        const float mn = m_new[e] == -INFINITY ? 0.f : m_new[e];
+        const float al = ex2_approx(m_run[e] - mn);
+        z_run[e] = z_run[e] * al + sum[e] * ex2_approx(ref[e] - mn);
+        o[e] *= al;
+        o[e + 2] *= al;
+#pragma unroll
+        for (int t = 0; t < NWC; ++t) rw[e][t] = ex2_approx(rw[e][t] - mn);
+        m_run[e] = m_new[e];
+      }
+    } else {
+      z_run[0] += sum[0];
+      z_run[1] += sum[1];
+    }
+    // O^T += V^T P^T; the matrix unit's sum covers this unit, the running one is fp32
+    const uint32_t vb = smem_u32(sm.stage[s]) + S::STAGE / 2 + vsub;
+    const uint32_t pb = smem_u32(&sm.P[buf][0][0][0]) + (uint32_t)xr * (PPITCH * 2) +
+                        (uint32_t)mi * 16u;
+    float acc[E::SPLIT][4];
+#pragma unroll
+    for (int t = 0; t < E::SPLIT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+#pragma unroll
+    for (int c2 = 0; c2 < CPW / 2; ++c2) {
+      uint32_t pf[E::SPLIT][4];  // two chunks' B fragments of each term
+#pragma unroll
+      for (int t = 0; t < E::SPLIT; ++t)
+        ldsm_x4(pb + (uint32_t)t * (GRP * PPITCH * 2) + (uint32_t)(th * CPW + 2 * c2) * 32u,
+                pf[t][0], pf[t][1], pf[t][2], pf[t][3]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int ch = th * CPW + 2 * c2 + u;
+        uint32_t vf[4];
+        ldsm_x4_trans(vb + tok_base(ch * 16), vf[0], vf[1], vf[2], vf[3]);
+#pragma unroll
+        for (int t = 0; t < E::SPLIT; ++t) E::mma(acc[t], vf, pf[t][2 * u], pf[t][2 * u + 1]);
+        if (moved) {  // each warp's weights are relative to their own maximum
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = 0.f;
+#pragma unroll
+            for (int t = E::SPLIT - 1; t >= 0; --t) {
+              v += acc[t][e];
+              acc[t][e] = 0.f;
+            }
+            // chunk ch was weighted by consumer warp ch
+            float f = 0.f;
+#pragma unroll
+            for (int t = 0; t < NWC; ++t) f = t == ch ? rw[e & 1][t] : f;
+            o[e] = fmaf(v, f, o[e]);
+          }
+        }
+      }
+    }
+    if (!moved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = 0.f;
+#pragma unroll
+        for (int t = E::SPLIT - 1; t >= 0; --t) v += acc[t][e];
+        o[e] += v;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[s]);
+
+    if (seg_end) {
+      // the lanes of a head hold parts of its Z; the warps' parts meet in zs
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        z_run[0] += __shfl_xor_sync(0xffffffffu, z_run[0], off);
+        z_run[1] += __shfl_xor_sync(0xffffffffu, z_run[1], off);
+      }
+      if (g4 == 0) {
+        sm.zs[cw][h0] = z_run[0];
+        sm.zs[cw][h1] = z_run[1];
+      }
+      const int d0 = dg * 16 + g4;
+      if (S::NTH > 1 && th == 1) {
+        sm.oh[h0 * HD + d0] = o[0];
+        sm.oh[h1 * HD + d0] = o[1];
+        sm.oh[h0 * HD + d0 + 8] = o[2];
+        sm.oh[h1 * HD + d0 + 8] = o[3];
+      }
+      named_bar_sync(BAR_ID, NTC);
+      if (th == 0) {
+        if (S::NTH > 1) {
+          o[0] += sm.oh[h0 * HD + d0];
+          o[1] += sm.oh[h1 * HD + d0];
+          o[2] += sm.oh[h0 * HD + d0 + 8];
+          o[3] += sm.oh[h1 * HD + d0 + 8];
+        }
+        float z[2] = {0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < NWC; ++t) {
+          z[0] += sm.zs[t][h0];
+          z[1] += sm.zs[t][h1];
+        }
+        const bool whole = seg_has_start && x.j == x.U - 1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int head = e ? h1 : h0;
+          if (whole) {
+            if (head >= p.r) continue;
+            const float rz = z[e] == 0.f ? 0.f : 1.f / z[e];
+            const size_t row = (size_t)x.b * p.Hq + (size_t)x.h * p.r + head;
+            p.out[row * HD + d0] = o[e] * rz;
+            p.out[row * HD + d0 + 8] = o[e + 2] * rz;
+            if (p.lse && dg == 0 && g4 == 0)
+              p.lse[row] = z[e] == 0.f ? -INFINITY
+                                       : (m_run[e] + (log2f(z[e]) - E::SHIFT)) * 0.69314718f;
+          } else {
+            float* slot = p.partials +
+                          (size_t)(2 * (int)blockIdx.x + (seg_has_start ? 1 : 0)) * S::SLOT;
+            slot[head * HD + d0] = o[e];
+            slot[head * HD + d0 + 8] = o[e + 2];
+            if (dg == 0 && g4 == 0) {
+              slot[GRP * HD + head] = m_run[e];
+              slot[GRP * HD + GRP + head] = z[e];
+            }
+          }
+        }
+      }
+      if (!(seg_has_start && x.j == x.U - 1)) {
+        // at most two a CTA: one that began before it, one that ends after it
+        const int start = sm.prefix[x.b] + x.h * x.U;
+        const int cf = unit_owner(start, total, G);
+        pend_b[npend] = x.b;
+        pend_h[npend] = x.h;
+        pend_first[npend] = cf;
+        pend_nc[npend] = unit_owner((long long)start + x.U - 1, total, G) - cf + 1;
+        ++npend;
+      }
+    }
+    advance(sm.prefix, p.B, p.Hkv, x);
+  }
+  if (npend) {
+    // tickets: the CTA that brings a head's count to its contributors joins it.
+    // A head's ticket is that of the CTA that holds its first unit.
+    __threadfence();
+    named_bar_sync(BAR_ID, NTC);
+    if (ct == 0) {
+      for (int e = 0; e < npend; ++e) {
+        uint32_t* tk = p.tickets + pend_first[e];
+        const bool last = atomic_add_acq_rel_gpu(tk, 1u) == (uint32_t)pend_nc[e] - 1u;
+        if (last) *tk = 0u;  // ready for the next call
+        sm.last[e] = last;
+      }
+      __threadfence();
+    }
+    named_bar_sync(BAR_ID, NTC);
+    for (int e = 0; e < npend; ++e)
+      if (sm.last[e])
+        join_partials<HD>(p, sm, pend_b[e], pend_h[e], pend_first[e], pend_nc[e], E::SHIFT, ct);
+  }
+  if (*abort_flag && ct == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
+}
+
+// ----------------------------------------------------------------- select
+
+constexpr int NT_SEL = 256;
+constexpr int NW_SEL = NT_SEL / 32;
+constexpr int MAX_CS = 8;  // CTAs per cluster (portable limit)
+
+struct SelectParams {
+  const void* q;
+  const void* means;
+  const int32_t* table;
+  const int32_t* seqlens;
+  int32_t* idx;
+  uint32_t* status;
+  int B, Hq, Hkv, r, k, sink, recent;
+  int ps_log2, num_pages, max_pages;
+  int ppc;       // pages of a CTA, at most
+  double scale;  // softmax scale
+};
+
+struct SelectSmem {
+  double wm[NW_SEL][GRP], wz[NW_SEL][GRP];
+  double cm[MAX_CS][GRP], cz[MAX_CS][GRP];  // each CTA's maxima and sums, sent by the peers
+  double m[GRP], f[GRP];
+  int hist[256];
+  int misc[4];
+  int wcnt[NW_SEL];
+  uint64_t sel[HYLRA_MAX_TOPK];
+};
+
+// dynamic shared memory: SelectSmem, e[r][ppc] doubles, keys[max_pages] (rank 0's are used)
+inline __host__ __device__ size_t select_smem(int r, int ppc, int max_pages) {
+  return sizeof(SelectSmem) + (size_t)r * ppc * 8 + (size_t)max_pages * 4;
+}
+
+// 16-bit elements to double (exact)
+template <typename T>
+__device__ __forceinline__ void widen2(uint32_t u, double& lo, double& hi) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    lo = (double)__uint_as_float(u << 16);
+    hi = (double)__uint_as_float(u & 0xffff0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    lo = (double)f.x;
+    hi = (double)f.y;
+  }
+}
+
+__device__ __forceinline__ void dmma_8x8x4(double (&d)[2], double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+               : "+d"(d[0]), "+d"(d[1])
+               : "d"(a), "d"(b));
+}
+
+// The kr largest (key, page) of keys[0..nc), key descending and index
+// ascending, sorted, into dst (as first + index).  kr <= nc.
+__device__ void select_top(const uint32_t* keys, SelectSmem& sm, int nc, int kr, int first,
+                           int32_t* dst) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int P2 = 1;
+  while (P2 < kr) P2 <<= 1;
+  for (int i = tid; i < P2; i += NT_SEL) sm.sel[i] = 0ull;
+  if (tid == 0) sm.misc[2] = 0;
+  // radix select on the bit patterns (scores are >= 0: unsigned order is numeric)
+  uint32_t prefix = 0;
+  int remain = kr, shift = 32;
+  bool whole = kr == nc;  // every key at the threshold digit is taken
+  while (!whole && shift > 0) {
+    shift -= 8;
+    sm.hist[tid] = 0;
+    __syncthreads();
+    for (int i0 = 0; i0 < nc; i0 += NT_SEL) {
+      const int i = i0 + tid;
+      const uint32_t key = i < nc ? keys[i] : 0u;
+      const bool in = i < nc && (shift == 24 || ((key ^ prefix) >> (shift + 8)) == 0u);
+      const uint32_t digit = in ? ((key >> shift) & 255u) : 256u;
+      const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+      if (in && (__ffs(peers) - 1) == lane) atomicAdd(&sm.hist[digit], __popc(peers));
+    }
+    __syncthreads();
+    if (wid == 0) {
+      int cnt[8], local = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cnt[i] = sm.hist[255 - 8 * lane - i];
+        local += cnt[i];
+      }
+      int incl = local;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      int acc = incl - local;
+      if (acc < remain && remain <= incl) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (acc < remain && remain <= acc + cnt[i]) {
+            sm.misc[0] = 255 - 8 * lane - i;
+            sm.misc[1] = remain - acc;
+            sm.misc[3] = cnt[i];
+          }
+          acc += cnt[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sm.misc[0] << shift;
+    remain = sm.misc[1];
+    whole = sm.misc[3] == remain;
+    __syncthreads();
+  }
+  __syncthreads();
+  const bool all = kr == nc;
+  const uint32_t tau = all ? 0u : prefix >> shift;
+  int before = 0;  // equal keys at lower indices
+  for (int i0 = 0; i0 < nc; i0 += NT_SEL) {
+    const int i = i0 + tid;
+    const uint32_t key = i < nc ? keys[i] : 0u;
+    const uint32_t top = all ? 1u : key >> shift;
+    bool take = i < nc && top > tau;
+    const bool eq = i < nc && top == tau;
+    if (whole) {
+      take |= eq;
+    } else {
+      // equal keys beyond the wanted number: the lowest indices
+      const uint32_t mask = __ballot_sync(0xffffffffu, eq);
+      if (lane == 0) sm.wcnt[wid] = __popc(mask);
+      __syncthreads();
+      int mine = before + __popc(mask & ((1u << lane) - 1u)), sum = 0;
+#pragma unroll
+      for (int w = 0; w < NW_SEL; ++w) {
+        if (w < wid) mine += sm.wcnt[w];
+        sum += sm.wcnt[w];
+      }
+      take |= eq && mine < remain;
+      before += sum;
+      __syncthreads();
+    }
+    if (take) {
+      const int at = atomicAdd(&sm.misc[2], 1);
+      if (at < kr) sm.sel[at] = ((uint64_t)key << 32) | (uint32_t)~(uint32_t)i;
+    }
+  }
+  __syncthreads();
+  // bitonic sort, descending; empty places are 0, below every entry
+  for (int k = 2; k <= P2; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int t = tid; t < P2 / 2; t += NT_SEL) {
+        const int i = 2 * t - (t & (j - 1));
+        const uint64_t a = sm.sel[i], b = sm.sel[i + j];
+        const bool desc = (i & k) == 0;
+        if (desc ? a < b : a > b) {
+          sm.sel[i] = b;
+          sm.sel[i + j] = a;
+        }
+      }
+      __syncthreads();
+    }
+  for (int i = tid; i < kr; i += NT_SEL)
+    dst[i] = first + (int32_t)~(uint32_t)(sm.sel[i] & 0xffffffffull);
+}
+
+template <int HD, typename T>
+__global__ void __launch_bounds__(NT_SEL)
+    paged_select_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) uint8_t smem_sel[];
+  SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_sel);
+  double* e = reinterpret_cast<double*>(smem_sel + sizeof(SelectSmem));  // [r][ppc]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(e + (size_t)p.r * p.ppc);
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int cs = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster per (b, h)
+  const int bh = (int)blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  cluster_arrive_relaxed();
+  griddep_wait();
+  griddep_launch_dependents();
+  const int psl = p.ps_log2;
+  const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, h == 0 && rank == 0 && tid == 0);
+  const int nb = (n + (1 << psl) - 1) >> psl;
+  const int c0 = min(p.sink, nb);              // pages [c0, c1) are ranked
+  const int c1 = max(c0, nb - p.recent);
+  const int nc = c1 - c0, forced = nb - nc;
+  const int kp = min(p.k, nb);
+  const int kr = max(0, kp - forced);
+  int32_t* dst = p.idx + (size_t)bh * p.k;
+  if (rank == 0) {
+    for (int i = tid; i < p.k; i += NT_SEL) {
+      if (i < min(forced, kp)) dst[i] = i < c0 ? i : c1 + (i - c0);
+      else if (i >= kp) dst[i] = -1;
+    }
+  }
+  if (kr == 0) {  // the same in every CTA of the cluster
+    cluster_wait_acquire();
+    return;
+  }
+  const int per = (nc + cs - 1) / cs;
+  const int s0 = min(nc, rank * per), s1 = min(nc, s0 + per), np = s1 - s0;
+
+  // logits on the 64-bit matrix unit: 8 pages x 8 heads, lane l holds the dims
+  // (l % 4) * HD/4 .. of page l / 4 and of head l / 4
+  constexpr int DL = HD / 4;
+  const int row = lane >> 2, c = lane & 3;
+  double qd[DL];
+  {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        static_cast<const T*>(p.q) + ((size_t)b * p.Hq + (size_t)h * p.r + min(row, p.r - 1)) * HD +
+        c * DL);
+#pragma unroll
+    for (int t = 0; t < DL / 8; ++t) {
+      const uint4 u = reinterpret_cast<const uint4*>(src)[t];
+      widen2<T>(u.x, qd[8 * t], qd[8 * t + 1]);
+      widen2<T>(u.y, qd[8 * t + 2], qd[8 * t + 3]);
+      widen2<T>(u.z, qd[8 * t + 4], qd[8 * t + 5]);
+      widen2<T>(u.w, qd[8 * t + 6], qd[8 * t + 7]);
+    }
+    if (row >= p.r)
+#pragma unroll
+      for (int t = 0; t < DL; ++t) qd[t] = 0.0;
+  }
+  double mx[2] = {-INFINITY, -INFINITY};
+  for (int g0 = wid * 8; g0 < np; g0 += NW_SEL * 8) {
+    const int at = g0 + row;
+    int pg = -1;
+    if (at < np) {
+      pg = __ldcg(p.table + (size_t)b * p.max_pages + c0 + s0 + at);
+      if (pg < 0 || pg >= p.num_pages) {
+        pg = -1;
+        atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+      }
+    }
+    double acc[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+    uint4 u[DL / 8];
+#pragma unroll
+    for (int t = 0; t < DL / 8; ++t) {
+      u[t] = make_uint4(0u, 0u, 0u, 0u);
+      if (pg >= 0)
+        u[t] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.means) +
+                                              ((size_t)pg * p.Hkv + h) * HD + c * DL)[t];
+    }
+#pragma unroll
+    for (int t = 0; t < DL / 8; ++t) {
+      const uint32_t v[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        double x0, x1;
+        widen2<T>(v[s], x0, x1);
+        dmma_8x8x4(acc[0], x0, qd[8 * t + 2 * s]);
+        dmma_8x8x4(acc[1], x1, qd[8 * t + 2 * s + 1]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const double l = pg >= 0 ? (acc[0][j] + acc[1][j]) * p.scale : -INFINITY;
+      if (at < np && 2 * c + j < p.r) e[(size_t)(2 * c + j) * p.ppc + at] = l;
+      mx[j] = fmax(mx[j], at < np ? l : -INFINITY);
+    }
+  }
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    mx[0] = fmax(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+    mx[1] = fmax(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+  }
+  if (row == 0) {
+    sm.wm[wid][2 * c] = mx[0];
+    sm.wm[wid][2 * c + 1] = mx[1];
+  }
+  __syncthreads();
+  if (tid < p.r) {
+    double m = sm.wm[0][tid];
+    for (int w = 1; w < NW_SEL; ++w) m = fmax(m, sm.wm[w][tid]);
+    sm.m[tid] = m;
+  }
+  __syncthreads();
+  // e = exp(logit - this CTA's maximum), and its sum
+  for (int g = 0; g < p.r; ++g) {
+    const double m = sm.m[g] == -INFINITY ? 0.0 : sm.m[g];
+    double z = 0.0;
+    for (int i = tid; i < np; i += NT_SEL) {
+      const double v = exp(e[(size_t)g * p.ppc + i] - m);
+      e[(size_t)g * p.ppc + i] = v;
+      z += v;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    if (lane == 0) sm.wz[wid][g] = z;
+  }
+  __syncthreads();
+  cluster_wait_acquire();  // every CTA of the cluster runs: its shared memory may be written
+  if (tid < cs * GRP) {
+    const int peer = tid / GRP, g = tid % GRP;
+    if (g < p.r) {
+      double z = 0.0;
+      for (int w = 0; w < NW_SEL; ++w) z += sm.wz[w][g];
+      st_dsmem_f64(mapa_shared(smem_u32(&sm.cm[rank][g]), peer), sm.m[g]);
+      st_dsmem_f64(mapa_shared(smem_u32(&sm.cz[rank][g]), peer), z);
+    }
+  }
+  cluster_sync_all();
+  if (tid < p.r) {
+    double M = -INFINITY, Z = 0.0;
+    for (int t = 0; t < cs; ++t) M = fmax(M, sm.cm[t][tid]);
+    for (int t = 0; t < cs; ++t)
+      if (sm.cm[t][tid] != -INFINITY) Z += sm.cz[t][tid] * exp(sm.cm[t][tid] - M);
+    sm.f[tid] = sm.m[tid] == -INFINITY ? 0.0 : exp(sm.m[tid] - M) / Z;
+  }
+  __syncthreads();
+  const uint32_t kbase = mapa_shared(smem_u32(keys), 0);
+  bool odd = false;
+  for (int i = tid; i < np; i += NT_SEL) {
+    double s = 0.0;
+    for (int g = 0; g < p.r; ++g) s += e[(size_t)g * p.ppc + i] * sm.f[g];
+    float key = (float)s;
+    if (!(key >= 0.f && key < INFINITY)) {
+      key = 0.f;
+      odd = true;
+    }
+    st_dsmem_u32(kbase + (uint32_t)(s0 + i) * 4u, __float_as_uint(key));
+  }
+  if (odd) atomicOr(p.status, HYLRA_STATUS_NONFINITE);
+  cluster_sync_all();
+  if (rank == 0) select_top(keys, sm, nc, kr, c0, dst + forced);
+}
+
+// ----------------------------------------------------------------- append
+
+constexpr int NT_APP = 256;
+constexpr int TILE_APP = 64;  // tokens per CTA, at most
+
+struct AppendParams {
+  const uint16_t* K_new;
+  const uint16_t* V_new;
+  const int32_t* slots;
+  uint16_t* K;
+  uint16_t* V;
+  uint16_t* means;  // may be null
+  uint32_t* status;
+  long long new_stride, page_stride, head_stride, token_stride;
+  int tokens, tile, Hkv, ps_log2, num_slots;
+};
+
+// grid (token tiles, KV heads).  A CTA copies its tokens' rows of one head; a
+// token in the last row of its page makes the page full, and the CTA then
+// averages the page: rows of this call from the new keys (the tokens before
+// it, whose slots count down by one), earlier rows from the pool.
+template <int HD, typename T>
+__global__ void __launch_bounds__(NT_APP)
+    paged_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int VPR = HD / 8;          // 16-byte vectors per row
+  constexpr int RP = NT_APP / VPR;     // rows at a time
+  __shared__ int slot_s[TILE_APP];
+  __shared__ float part[NT_APP][9];    // 9: threads of a column land in different banks
+  __shared__ bool fresh[UTOK];         // rows of a full page that this call brings
+  const int tid = threadIdx.x, v = tid % VPR, rl = tid / VPR;
+  const int h = (int)blockIdx.y, t0 = (int)blockIdx.x * p.tile;
+  const int cnt = min(p.tile, p.tokens - t0);
+  const int ps = 1 << p.ps_log2;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int i = tid; i < cnt; i += NT_APP) {
+    int s = __ldcg(p.slots + t0 + i);
+    if (s < 0 || s >= p.num_slots) {
+      if (s != -1 && h == 0) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+      s = -1;
+    }
+    slot_s[i] = s;
+  }
+  __syncthreads();
+  for (int i = rl; i < cnt; i += RP) {
+    const int s = slot_s[i];
+    if (s < 0) continue;
+    const size_t src = (size_t)(t0 + i) * p.new_stride + (size_t)h * HD + v * 8;
+    const size_t dst = (size_t)(s >> p.ps_log2) * p.page_stride + (size_t)h * p.head_stride +
+                       (size_t)(s & (ps - 1)) * p.token_stride + v * 8;
+    const uint4 kv = *reinterpret_cast<const uint4*>(p.K_new + src);
+    const uint4 vv = *reinterpret_cast<const uint4*>(p.V_new + src);
+    *reinterpret_cast<uint4*>(p.K + dst) = kv;
+    *reinterpret_cast<uint4*>(p.V + dst) = vv;
+  }
+  if (!p.means) return;
+  for (int i = 0; i < cnt; ++i) {
+    const int s = slot_s[i];  // the same in every thread
+    if (s < 0 || (s & (ps - 1)) != ps - 1) continue;
+    const int t = t0 + i, page = s >> p.ps_log2;
+    // row ps-1-back is new if the token `back` places before t has its slot
+    if (tid < ps) {
+      const int back = ps - 1 - tid;
+      fresh[tid] = t >= back && __ldcg(p.slots + t - back) == s - back;
+    }
+    __syncthreads();
+    float sum[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+    for (int row = rl; row < ps; row += RP) {
+      const uint16_t* src =
+          fresh[row] ? p.K_new + (size_t)(t - (ps - 1 - row)) * p.new_stride + (size_t)h * HD
+                     : p.K + (size_t)page * p.page_stride + (size_t)h * p.head_stride +
+                           (size_t)row * p.token_stride;
+      const uint4 u = *reinterpret_cast<const uint4*>(src + v * 8);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum[2 * k] += Elem<T>::value((uint16_t)(w[k] & 0xffffu));
+        sum[2 * k + 1] += Elem<T>::value((uint16_t)(w[k] >> 16));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[tid][k] = sum[k];
+    __syncthreads();
+    if (tid < HD) {
+      float total = 0.f;
+      for (int q = 0; q < RP; ++q) total += part[q * VPR + tid / 8][tid % 8];
+      p.means[((size_t)page * p.Hkv + h) * HD + tid] = Elem<T>::bits(total / (float)ps);
+    }
+    __syncthreads();
+  }
+}
+
+// ----------------------------------------------------------------- tables
+
+constexpr int NT_TAB = 256;
+
+struct TablesParams {
+  const int32_t* cached;
+  const int32_t* added;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* table;
+  int32_t* seqlens;
+  int32_t* cu;
+  int32_t* slots;
+  int32_t* free_left;
+  uint32_t* status;
+  uint32_t* ticket;
+  int B, ps_log2, num_pages, max_pages, free_cap, slot_cap;
+};
+
+struct TablesSmem {
+  int cu[MAX_B + 1];     // tokens before request b (saturating)
+  int first[MAX_B + 1];  // pages taken before request b
+  int held[MAX_B];       // cached tokens; -1: refused
+  long long wt[NT_TAB / 32];
+  int wp[NT_TAB / 32];
+  int free_n, left, last;
+};
+
+// Inclusive sums of (tokens, pages) over the block's threads.
+__device__ __forceinline__ void scan2(long long& t, int& a, TablesSmem& sm) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long vt = __shfl_up_sync(0xffffffffu, t, off);
+    const int va = __shfl_up_sync(0xffffffffu, a, off);
+    if (lane >= off) {
+      t += vt;
+      a += va;
+    }
+  }
+  if (lane == 31) {
+    sm.wt[wid] = t;
+    sm.wp[wid] = a;
+  }
+  __syncthreads();
+  for (int w = 0; w < wid; ++w) {
+    t += sm.wt[w];
+    a += sm.wp[w];
+  }
+}
+
+// Every CTA derives the running sums for itself (a few thousand bytes), then
+// writes its share of slots and table entries; the last CTA to have read the
+// inputs writes the small outputs, which may be the inputs themselves.
+__global__ void __launch_bounds__(NT_TAB)
+    paged_tables_kernel(const __grid_constant__ TablesParams p) {
+  __shared__ TablesSmem sm;
+  constexpr int PER = MAX_B / NT_TAB;  // requests per thread
+  const int tid = threadIdx.x, psl = p.ps_log2, ps = 1 << psl;
+  const bool report = blockIdx.x == 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (tid == 0) {
+    int f = __ldcg(p.free_count);
+    if (f < 0 || f > p.free_cap) {
+      if (report) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+      f = 0;
+    }
+    sm.free_n = f;
+  }
+  int held[PER], add[PER], need[PER];
+  bool bad[PER];
+  long long tsum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    held[i] = add[i] = need[i] = 0;
+    bad[i] = false;
+    if (b < p.B) {
+      held[i] = __ldcg(p.cached + b);
+      add[i] = __ldcg(p.added + b);
+      const int cap = p.max_pages << psl;
+      bad[i] = held[i] < 0 || add[i] < 0 || held[i] > cap || add[i] > cap - held[i];
+      if (add[i] < 0) add[i] = 0;
+    }
+    tsum += add[i];
+  }
+  long long tend = tsum;
+  int dummy = 0;
+  scan2(tend, dummy, sm);
+  long long trun = tend - tsum;
+  int psum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    if (b < p.B) sm.cu[b] = (int)min(trun, (long long)INT32_MAX);
+    trun += add[i];
+    if (b == p.B - 1) sm.cu[p.B] = (int)min(trun, (long long)INT32_MAX);
+    if (b < p.B && trun > p.slot_cap && add[i] > 0) bad[i] = true;
+    if (b < p.B && !bad[i])
+      need[i] = ((held[i] + add[i] + ps - 1) >> psl) - ((held[i] + ps - 1) >> psl);
+    psum += need[i];
+  }
+  __syncthreads();
+  long long tdummy = 0;
+  int pend = psum;
+  scan2(tdummy, pend, sm);
+  int prun = pend - psum;
+  const int avail = sm.free_n;
+  if (tid == 0) sm.left = avail;
+  __syncthreads();
+  uint32_t bits = 0;
+  int taken = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    if (b < p.B) {
+      sm.first[b] = prun;
+      prun += need[i];
+      const bool full = need[i] > 0 && prun > avail;
+      if (bad[i]) bits |= HYLRA_STATUS_BAD_SEQLEN;
+      if (full) bits |= HYLRA_STATUS_NO_PAGES;
+      else taken += need[i];
+      sm.held[b] = bad[i] || full ? -1 : held[i];
+      if (b == p.B - 1) sm.first[p.B] = prun;
+    }
+  }
+  if (taken) atomicSub(&sm.left, taken);
+  if (bits && report) atomicOr(p.status, bits);
+  __syncthreads();
+  const int left = sm.left, used = avail - left, cu_end = sm.cu[p.B];
+
+  auto owner = [&](const int* start, int i) {  // last request whose start is <= i
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  auto popped = [&](int nth) {
+    const int pg = __ldcg(p.free_pages + (avail - 1 - nth));
+    return pg >= 0 && pg < p.num_pages ? pg : -1;
+  };
+  const int step = (int)gridDim.x * NT_TAB;
+  bool odd = false;
+  for (int a = (int)blockIdx.x * NT_TAB + tid; a < used; a += step) {
+    const int b = owner(sm.first, a);
+    const int pg = popped(a);
+    odd |= pg < 0;
+    p.table[(size_t)b * p.max_pages + ((sm.held[b] + ps - 1) >> psl) + (a - sm.first[b])] = pg;
+  }
+  for (long long tl = (long long)blockIdx.x * NT_TAB + tid; tl < p.slot_cap; tl += step) {
+    const int t = (int)tl;
+    int slot = -1;
+    if (t < cu_end) {
+      const int b = owner(sm.cu, t);
+      if (sm.held[b] >= 0) {
+        const int pos = sm.held[b] + (t - sm.cu[b]), j = pos >> psl;
+        const int have = (sm.held[b] + ps - 1) >> psl;
+        int pg;
+        if (j < have) {
+          pg = __ldcg(p.table + (size_t)b * p.max_pages + j);
+          if (pg < 0 || pg >= p.num_pages) pg = -1;
+        } else {
+          pg = popped(sm.first[b] + j - have);
+        }
+        odd |= pg < 0;
+        if (pg >= 0) slot = (pg << psl) + (pos & (ps - 1));
+      }
+    }
+    p.slots[t] = slot;
+  }
+  if (odd) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
+      const bool last = atomic_add_acq_rel_gpu(p.ticket, 1u) == gridDim.x - 1;
+      if (last) *p.ticket = 0u;
+      sm.last = last;
+    }
+    __syncthreads();
+    if (!sm.last) return;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int b = tid * PER + i;
+    if (b < p.B) {
+      p.cu[b] = sm.cu[b];
+      p.seqlens[b] = sm.held[b] >= 0 ? held[i] + add[i] : held[i];
+    }
+  }
+  if (tid == 0) {
+    p.cu[p.B] = cu_end;
+    *p.free_left = left;
+  }
+}
+
+}  // namespace paged
+}  // namespace hylra

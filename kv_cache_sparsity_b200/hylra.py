@@ -27,12 +27,14 @@ MAX_SEQLEN = 262144
 
 BF16 = 0
 FP32 = 1
+FP16 = 2  # paged calls only
 
 STATUS_BAD_SEQLEN = 0x1
 STATUS_BAD_INDEX = 0x2
 STATUS_DUP_INDEX = 0x4
 STATUS_NONFINITE = 0x8
 STATUS_TIMEOUT = 0x10
+STATUS_NO_PAGES = 0x20
 
 ERRORS = {0: "HYLRA_OK", -1: "HYLRA_ERR_INVALID", -2: "HYLRA_ERR_UNSUPPORTED",
           -3: "HYLRA_ERR_CUDA", -4: "HYLRA_ERR_WORKSPACE"}
@@ -44,7 +46,9 @@ EXPORTS = ("hylra_workspace_bytes", "hylra_workspace_init", "hylra_decode_full",
            "hylra_stage_bytes", "hylra_gather_blocks", "hylra_decode_reuse_staged",
            "hylra_decode_step_offload", "hylra_overlap_counts",
            "hylra_similarity_from_counts", "hylra_set_wait_limit", "hylra_token_scores",
-           "hylra_token_topk")
+           "hylra_token_topk", "hylra_paged_workspace_bytes", "hylra_paged_tables",
+           "hylra_paged_append", "hylra_paged_decode", "hylra_paged_select",
+           "hylra_paged_decode_topk")
 
 
 class HylraError(RuntimeError):
@@ -62,6 +66,17 @@ class Shape(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("max_seqlen", ctypes.c_int32),
                 ("kv_capacity", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
                 ("seq_offsets", ctypes.c_void_p)]
+
+
+class PagedShape(ctypes.Structure):
+    """Mirror of hylra_paged_t."""
+
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float)]
 
 
 def make_shape(batch, num_q_heads, num_kv_heads, topk, max_seqlen, dtype=BF16, kv_capacity=0,
@@ -86,7 +101,7 @@ def load() -> ctypes.CDLL:
                            "`python -m kv_cache_sparsity_b200.build`")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, I32, I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
-    SP = ctypes.POINTER(Shape)
+    SP, PP = ctypes.POINTER(Shape), ctypes.POINTER(PagedShape)
     sig = {
         "hylra_workspace_bytes": [SP, ctypes.POINTER(ctypes.c_size_t)],
         "hylra_workspace_init": [P, S, P],
@@ -109,6 +124,12 @@ def load() -> ctypes.CDLL:
         "hylra_set_wait_limit": [I64],
         "hylra_token_scores": [SP, P, P, P, P, P, P, P, P, S, P],
         "hylra_token_topk": [I32, I32, P, P, I32, P],
+        "hylra_paged_workspace_bytes": [PP, ctypes.POINTER(ctypes.c_size_t)],
+        "hylra_paged_tables": [PP, P, P, P, I32, P, P, P, P, P, I32, P, P, S, P],
+        "hylra_paged_append": [PP, P, P, I64, P, I32, P, P, P, P, S, P],
+        "hylra_paged_decode": [PP, P, P, P, P, P, P, P, P, S, P],
+        "hylra_paged_select": [PP, P, P, P, P, I32, I32, I32, P, P, S, P],
+        "hylra_paged_decode_topk": [PP, P, P, P, P, P, P, I32, P, P, P, S, P],
         "hylra_strerror": [ctypes.c_int],
         "hylra_version": [],
     }
@@ -330,3 +351,173 @@ def decode_step_offload(shape: Shape, policy: Sequence[int], qs, Ks, Vs, offload
                                             _ptr(V_stage), _ptr(ws),
                                             ws.numel() * ws.element_size(), _stream(stream)),
            "hylra_decode_step_offload")
+
+
+# ------------------------------------------------------------- paged cache
+#
+# Device buffers are torch CUDA tensors of one device; the calls run on that
+# device's current stream unless given another.  A tensor of the wrong type,
+# shape or layout raises ValueError before the library is called.
+
+
+def make_paged_shape(batch, num_q_heads, num_kv_heads, page_size, num_pages, max_pages,
+                     dtype=BF16, head_dim=HEAD_DIM, pool=None, scale=0.0) -> PagedShape:
+    """Build a PagedShape.  ``pool``: the K pool as a [num_pages, num_kv_heads,
+    page_size, head_dim] tensor of any strides (the V pool has the same), for
+    example ``pages.transpose(1, 2)`` of a [page, row, head, d] array; without
+    it the pools are contiguous in that order.  ``scale`` 0: 1/sqrt(head_dim)."""
+    strides = (num_kv_heads * page_size * head_dim, page_size * head_dim, head_dim)
+    if pool is not None:
+        want = (num_pages, num_kv_heads, page_size, head_dim)
+        if tuple(pool.shape) != want:
+            raise ValueError(f"pool: shape {tuple(pool.shape)}, expected {want}")
+        if pool.stride(3) != 1:
+            raise ValueError("pool: the elements of a row must be adjacent")
+        strides = pool.stride()[:3]
+    return PagedShape(batch, num_q_heads, num_kv_heads, head_dim, page_size, dtype, num_pages,
+                      max_pages, *strides, scale)
+
+
+def paged_workspace_bytes(shape: PagedShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hylra_paged_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)),
+           "hylra_paged_workspace_bytes")
+    return n.value
+
+
+def _type_of(shape: PagedShape):
+    import torch
+    return torch.bfloat16 if shape.dtype == BF16 else torch.float16
+
+
+def _want(what, t, dtype, shape, dev, dense=True):
+    """Raise unless t is a tensor of this type and shape on device index dev (contiguous if dense)."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{dev}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+
+
+def _want_pools(s: PagedShape, K, V, dev):
+    shape = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)
+    strides = (s.page_stride, s.head_stride, s.token_stride, 1)
+    for what, t in (("K_pages", K), ("V_pages", V)):
+        _want(what, t, _type_of(s), shape, dev, dense=False)
+        # the stride of a dimension of one element has no meaning
+        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
+            raise ValueError(f"{what}: strides {t.stride()} differ from the shape's {strides}")
+
+
+def _paged_call(name, ws, stream, *args):
+    """args -> the entry point, with the workspace and the stream, on the workspace's device."""
+    import torch
+    dev = ws.get_device()
+    if dev < 0 or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous CUDA tensor")
+    f = getattr(load(), name)
+    nbytes = ws.numel() * ws.element_size()
+    if dev == torch.cuda.current_device():
+        rc = f(*args, ws.data_ptr(), nbytes, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, ws.data_ptr(), nbytes, _stream(stream))
+    if rc:
+        raise HylraError(rc, name)
+
+
+def paged_tables(shape: PagedShape, cached_lens, new_lens, free_pages, free_count, block_table,
+                 seqlens_out, cu_new, slot_map, free_count_out, ws, stream=None):
+    """Pages, slots and lengths of a step's new tokens (all int32)."""
+    import torch
+    dev, B, i32 = ws.get_device(), shape.batch, torch.int32
+    for what, t, n in (("cached_lens", cached_lens, B), ("new_lens", new_lens, B),
+                       ("free_count", free_count, 1), ("seqlens_out", seqlens_out, B),
+                       ("cu_new", cu_new, B + 1), ("free_count_out", free_count_out, 1),
+                       ("free_pages", free_pages, free_pages.numel()),
+                       ("slot_map", slot_map, slot_map.numel())):
+        _want(what, t, i32, (n,), dev)
+    _want("block_table", block_table, i32, (B, shape.max_pages), dev)
+    _paged_call("hylra_paged_tables", ws, stream, ctypes.byref(shape), cached_lens.data_ptr(),
+                new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+                free_count.data_ptr(), block_table.data_ptr(), seqlens_out.data_ptr(),
+                cu_new.data_ptr(), slot_map.data_ptr(), slot_map.numel(),
+                free_count_out.data_ptr())
+
+
+def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, key_means, ws,
+                 stream=None):
+    """K_new / V_new [T, Hkv, d] (each token's heads adjacent, tokens at any stride) into the
+    pools; key_means [num_pages, Hkv, d] or None."""
+    import torch
+    dev, t = ws.get_device(), _type_of(shape)
+    n, H, d = slot_map.numel(), shape.num_kv_heads, shape.head_dim
+    _want("slot_map", slot_map, torch.int32, (n,), dev)
+    for what, x in (("K_new", K_new), ("V_new", V_new)):
+        _want(what, x, t, (n, H, d), dev, dense=False)
+        if n and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
+            raise ValueError(f"{what}: a token's heads must be adjacent")
+    stride = K_new.stride(0) if n > 1 else H * d
+    if n > 1 and V_new.stride(0) != stride:
+        raise ValueError("K_new and V_new must have the same token stride")
+    _want_pools(shape, K_pages, V_pages, dev)
+    if key_means is not None:
+        _want("key_means", key_means, t, (shape.num_pages, H, d), dev)
+    _paged_call("hylra_paged_append", ws, stream, ctypes.byref(shape), K_new.data_ptr(),
+                V_new.data_ptr(), stride, slot_map.data_ptr(), n, K_pages.data_ptr(),
+                V_pages.data_ptr(), _ptr(key_means))
+
+
+def _want_query(s: PagedShape, q, block_table, seqlens, dev):
+    import torch
+    _want("q", q, _type_of(s), (s.batch, s.num_q_heads, s.head_dim), dev)
+    _want("block_table", block_table, torch.int32, (s.batch, s.max_pages), dev)
+    _want("seqlens", seqlens, torch.int32, (s.batch,), dev)
+
+
+def _want_result(s: PagedShape, out, lse, dev):
+    import torch
+    _want("out", out, torch.float32, (s.batch, s.num_q_heads, s.head_dim), dev)
+    if lse is not None:
+        _want("lse", lse, torch.float32, (s.batch, s.num_q_heads), dev)
+
+
+def paged_decode(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, out, ws, lse=None,
+                 stream=None):
+    """Attention of one query token per sequence over its pages; lse: fp32 [B, Hq] or None."""
+    dev = ws.get_device()
+    _want_query(shape, q, block_table, seqlens, dev)
+    _want_pools(shape, K_pages, V_pages, dev)
+    _want_result(shape, out, lse, dev)
+    _paged_call("hylra_paged_decode", ws, stream, ctypes.byref(shape), q.data_ptr(),
+                K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+                seqlens.data_ptr(), out.data_ptr(), _ptr(lse))
+
+
+def paged_select(shape: PagedShape, q, key_means, block_table, seqlens, page_idx, ws, sink=1,
+                 recent=1, stream=None):
+    """The most promising pages of each (sequence, KV head) into page_idx int32 [B, Hkv, k]."""
+    import torch
+    dev, k = ws.get_device(), page_idx.shape[-1]
+    _want_query(shape, q, block_table, seqlens, dev)
+    _want("key_means", key_means, _type_of(shape),
+          (shape.num_pages, shape.num_kv_heads, shape.head_dim), dev)
+    _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
+    _paged_call("hylra_paged_select", ws, stream, ctypes.byref(shape), q.data_ptr(),
+                key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), k, sink, recent,
+                page_idx.data_ptr())
+
+
+def paged_decode_topk(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, page_idx, out,
+                      ws, lse=None, stream=None):
+    """paged_decode over the pages listed in page_idx int32 [B, Hkv, k]."""
+    import torch
+    dev, k = ws.get_device(), page_idx.shape[-1]
+    _want_query(shape, q, block_table, seqlens, dev)
+    _want_pools(shape, K_pages, V_pages, dev)
+    _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
+    _want_result(shape, out, lse, dev)
+    _paged_call("hylra_paged_decode_topk", ws, stream, ctypes.byref(shape), q.data_ptr(),
+                K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+                seqlens.data_ptr(), page_idx.data_ptr(), k, out.data_ptr(), _ptr(lse))

@@ -1,0 +1,150 @@
+"""Shared helpers of the paged-cache tests: small caches with hostile unused
+memory, the calls through the binding, and tolerances from the arithmetic."""
+
+from __future__ import annotations
+
+import dataclasses
+import math
+
+import numpy as np
+import torch
+
+from kv_cache_sparsity_b200 import hylra as H
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def f64(t: torch.Tensor) -> np.ndarray:
+    return t.detach().double().cpu().numpy()
+
+
+def pool_tensor(pages, heads, page, d, dtype, layout, device="cuda"):
+    """A [pages, heads, page, d] tensor in one of three memory layouts, filled with NaN."""
+    if layout == "hnd":
+        t = torch.empty(pages, heads, page, d, dtype=dtype, device=device)
+    elif layout == "nhd":
+        t = torch.empty(pages, page, heads, d, dtype=dtype, device=device).transpose(1, 2)
+    else:  # "slice": every second half of rows twice as long, in a pool of K and V pages
+        t = torch.empty(pages, 2, heads, page, 2 * d, dtype=dtype, device=device)[:, 1, :, :, d:]
+    return t.fill_(math.nan)
+
+
+@dataclasses.dataclass
+class Cache:
+    page: int
+    hq: int
+    hkv: int
+    d: int
+    dtype: str
+    lens: tuple
+    keys: torch.Tensor
+    vals: torch.Tensor
+    table: torch.Tensor
+    seqlens: torch.Tensor
+    q: torch.Tensor
+    shape: H.PagedShape
+    ws: torch.Tensor
+    scale: float
+
+    def status(self):
+        torch.cuda.synchronize()
+        return H.read_status(self.ws, clear=True)
+
+    def result(self):
+        B = len(self.lens)
+        return (torch.full((B, self.hq, self.d), math.nan, device="cuda"),
+                torch.full((B, self.hq), math.nan, device="cuda"))
+
+    def decode(self, **kw):
+        out, lse = self.result()
+        H.paged_decode(self.shape, self.q, self.keys, self.vals, self.table, self.seqlens, out,
+                       self.ws, lse=lse, **kw)
+        return out, lse
+
+    def decode_topk(self, idx, **kw):
+        out, lse = self.result()
+        H.paged_decode_topk(self.shape, self.q, self.keys, self.vals, self.table, self.seqlens,
+                            idx, out, self.ws, lse=lse, **kw)
+        return out, lse
+
+
+def workspace(shape):
+    ws = torch.empty(H.paged_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    H.workspace_init(ws)
+    return ws
+
+
+def make_cache(lens, page=16, hq=8, hkv=2, d=128, dtype="bf16", layout="hnd", seed=0, scale=0.0,
+               spare=3, cols=None, sharp=1.0):
+    """Random keys and values in randomly placed pages.  Rows past a sequence's
+    end, unused pages and unused table entries hold NaN and ids out of range."""
+    g = torch.Generator().manual_seed(seed)
+    t = DTYPES[dtype]
+    have = [-(-n // page) for n in lens]
+    pool = sum(have) + spare
+    cols = cols or max(1, max(have))
+    order = torch.randperm(pool, generator=g)
+    table = torch.full((len(lens), cols), 2**30, dtype=torch.int32)
+    keys = pool_tensor(pool, hkv, page, d, t, layout)
+    vals = pool_tensor(pool, hkv, page, d, t, layout)
+    at = 0
+    for b, n in enumerate(lens):
+        pages = order[at:at + have[b]]
+        at += have[b]
+        table[b, : have[b]] = pages.to(torch.int32)
+        for i, p in enumerate(pages.tolist()):
+            rows = min(page, n - i * page)
+            keys[p, :, :rows] = torch.randn(hkv, rows, d, generator=g).to(t).cuda()
+            vals[p, :, :rows] = torch.randn(hkv, rows, d, generator=g).to(t).cuda()
+    q = (sharp * torch.randn(len(lens), hq, d, generator=g)).to(t).cuda()
+    shape = H.make_paged_shape(len(lens), hq, hkv, page, pool, cols,
+                               dtype=H.BF16 if dtype == "bf16" else H.FP16, head_dim=d, pool=keys,
+                               scale=scale)
+    return Cache(page, hq, hkv, d, dtype, tuple(lens), keys, vals, table.cuda(),
+                 torch.tensor(lens, dtype=torch.int32, device="cuda"), q, shape, workspace(shape),
+                 scale or 1.0 / math.sqrt(d))
+
+
+def attention_tolerance(c: Cache):
+    """(largest error of an output element, of an lse) that the arithmetic allows.
+
+    A logit is a sum of d exact products in fp32.  Each addition of the matrix
+    unit may be off by one unit of the running sum (2^-23: it need not round to
+    nearest), so a logit is off by at most d * 2^-23 * S, S = the largest
+    scale * sum |q_i k_i|.  Subtracting the maximum and multiplying by the scale
+    in one fused step adds 2^-24 of a number below 2 S * log2(e), and the scale
+    itself is rounded to fp32: 3 S * 2^-24 more.  A weight exp(x) is then off
+    by that much, by 2^-22 (exponential) and by its split into 16-bit terms:
+    at most (eps/2)^3 = 2^-24 (three bf16 terms) or (eps/2)^2 = 2^-22 (two fp16
+    terms).  out = sum p v / sum p doubles the weights' part; the sums have at
+    most n additions of 2^-23 each, but run in tiles: 8 * 16 in the matrix unit,
+    then one a tile, 8 warps and 256 contributors.  The result is stored in
+    fp32 (2^-24), all times the largest |v|.  lse: the same once, plus the
+    logarithm's 2^-22 of a number below S + log n.
+    """
+    ok = [n for n in c.lens if n > 0]
+    if not ok:
+        return 0.0, 0.0
+    fin = lambda t: torch.nan_to_num(t.float(), nan=0.0).abs()  # noqa: E731
+    k, v = fin(c.keys).amax((0, 2)), float(fin(c.vals).max())
+    r = c.hq // c.hkv
+    S = float((c.q.float().abs().view(-1, c.hkv, r, c.d) * k[None, :, None]).sum(-1).max()) * c.scale
+    logit = c.d * 2.0**-23 * S + 3 * S * 2.0**-24 + 2 * 2.0**-24 * S * 1.4427
+    weight = logit + 2.0**-22 + 2.0**-22
+    adds = 128 + max(ok) / 128 + 8 + 256
+    out = v * (2 * weight + 2 * adds * 2.0**-23 + 2.0**-24)
+    return out, weight + adds * 2.0**-23 + (S + math.log(max(ok)) + 20) * 2.0**-22
+
+
+def check_attention(c: Cache, got, want, what=""):
+    (out, lse), (o_ref, l_ref) = got, want
+    tol_o, tol_l = attention_tolerance(c)
+    o, l = f64(out), f64(lse)
+    assert np.array_equal(np.isneginf(l), np.isneginf(l_ref)), what
+    assert np.isfinite(o).all(), what
+    live = np.isfinite(l_ref)
+    assert np.all(o[~live] == 0), what
+    err_o = float(np.abs(o - o_ref).max(initial=0.0))
+    err_l = float(np.abs(l[live] - l_ref[live]).max(initial=0.0))
+    assert err_o <= tol_o and err_l <= tol_l, (what, err_o, tol_o, err_l, tol_l)
+    return err_o, err_l

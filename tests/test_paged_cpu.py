@@ -1,0 +1,217 @@
+"""Paged-cache calls without a GPU: refusals before any launch, the binding's
+checks, and pins of the 64-bit oracle."""
+
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_sparsity_b200 import build as hbuild
+from kv_cache_sparsity_b200 import hylra as H
+from oracle import paged_oracle as O
+
+INVALID, UNSUPPORTED = -1, -2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    hbuild.build()
+    return H.load()
+
+
+def _shape(**kw):
+    strides = {k: kw.pop(k) for k in ("page_stride", "head_stride", "token_stride") if k in kw}
+    base = dict(batch=2, num_q_heads=8, num_kv_heads=2, page_size=16, num_pages=10, max_pages=5)
+    base.update(kw)
+    s = H.make_paged_shape(**base)
+    for k, v in strides.items():
+        setattr(s, k, v)
+    return s
+
+
+# a non-null, aligned address for arguments that a refused call never touches
+PTR = 1 << 20
+
+
+def _calls(lib, shape, **kw):
+    """Return codes of every entry point for this shape, with the given arguments changed."""
+    a = dict(q=PTR, K=PTR, V=PTR, table=PTR, lens=PTR, out=PTR, lse=None, ws=PTR, nbytes=1 << 30,
+             k=4, idx=PTR, means=PTR, sink=1, recent=1, new_stride=256, tokens=3, slots=PTR,
+             free_cap=5, slot_cap=5)
+    a.update(kw)
+    s = ctypes.byref(shape) if shape is not None else None
+    yield "tables", lib.hylra_paged_tables(s, a["lens"], a["lens"], a["slots"], a["free_cap"],
+                                           a["lens"], a["table"], a["lens"], a["lens"], a["slots"],
+                                           a["slot_cap"], a["lens"], a["ws"], a["nbytes"], None)
+    yield "append", lib.hylra_paged_append(s, a["K"], a["V"], a["new_stride"], a["slots"],
+                                           a["tokens"], a["K"], a["V"], a["means"], a["ws"],
+                                           a["nbytes"], None)
+    yield "decode", lib.hylra_paged_decode(s, a["q"], a["K"], a["V"], a["table"], a["lens"],
+                                           a["out"], a["lse"], a["ws"], a["nbytes"], None)
+    yield "select", lib.hylra_paged_select(s, a["q"], a["means"], a["table"], a["lens"], a["k"],
+                                           a["sink"], a["recent"], a["idx"], a["ws"], a["nbytes"],
+                                           None)
+    yield "topk", lib.hylra_paged_decode_topk(s, a["q"], a["K"], a["V"], a["table"], a["lens"],
+                                              a["idx"], a["k"], a["out"], a["lse"], a["ws"],
+                                              a["nbytes"], None)
+
+
+ALL = {"tables", "append", "decode", "select", "topk"}
+POOL = {"append", "decode", "topk"}
+
+
+@pytest.mark.parametrize("kw,code,who", [
+    (dict(batch=0), INVALID, ALL), (dict(batch=1025), UNSUPPORTED, ALL),
+    (dict(num_q_heads=0), INVALID, ALL), (dict(num_q_heads=7), INVALID, ALL),
+    (dict(num_kv_heads=0, num_q_heads=1), INVALID, ALL),
+    (dict(num_q_heads=18), UNSUPPORTED, ALL),
+    (dict(head_dim=96), UNSUPPORTED, ALL), (dict(head_dim=256), UNSUPPORTED, ALL),
+    (dict(page_size=8), UNSUPPORTED, ALL), (dict(page_size=48), UNSUPPORTED, ALL),
+    (dict(page_size=256), UNSUPPORTED, ALL), (dict(page_size=0), UNSUPPORTED, ALL),
+    (dict(dtype=H.FP32), UNSUPPORTED, ALL), (dict(dtype=5), INVALID, ALL),
+    (dict(num_pages=0), INVALID, ALL), (dict(max_pages=0), INVALID, ALL),
+    (dict(num_pages=1 << 27), UNSUPPORTED, ALL), (dict(max_pages=16385), UNSUPPORTED, ALL),
+    (dict(scale=-1.0), INVALID, ALL), (dict(scale=math.nan), INVALID, ALL),
+    (dict(scale=math.inf), INVALID, ALL),
+    (dict(num_q_heads=1 << 20, num_kv_heads=1 << 20), UNSUPPORTED, ALL),
+    (dict(page_stride=4096 - 8), INVALID, POOL), (dict(token_stride=120), INVALID, POOL),
+    (dict(token_stride=132), INVALID, POOL), (dict(head_stride=0), INVALID, POOL),
+    (dict(page_stride=-4096), INVALID, POOL), (dict(page_stride=1 << 39), UNSUPPORTED, POOL),
+])
+def test_shapes_refused(lib, kw, code, who):
+    s = _shape(**kw)
+    for name, rc in _calls(lib, s):
+        if name in who:
+            assert rc == code, name
+    if who is ALL:
+        n = ctypes.c_size_t(7)
+        assert lib.hylra_paged_workspace_bytes(ctypes.byref(s), ctypes.byref(n)) == code
+        assert n.value == 7
+
+
+@pytest.mark.parametrize("kw,code,who", [
+    (dict(q=0), INVALID, {"decode", "select", "topk"}), (dict(q=PTR + 8), INVALID, {"decode"}),
+    (dict(K=None), INVALID, POOL), (dict(V=PTR + 2), INVALID, POOL),
+    (dict(table=None), INVALID, {"tables", "decode", "select", "topk"}),
+    (dict(lens=PTR + 1), INVALID, {"tables", "decode", "select", "topk"}),
+    (dict(out=None), INVALID, {"decode", "topk"}), (dict(lse=PTR + 2), INVALID, {"decode"}),
+    (dict(k=0), INVALID, {"select", "topk"}), (dict(k=1025), UNSUPPORTED, {"select", "topk"}),
+    (dict(idx=None), INVALID, {"select", "topk"}), (dict(sink=-1), INVALID, {"select"}),
+    (dict(recent=0), INVALID, {"select"}), (dict(means=None), INVALID, {"select"}),
+    (dict(means=PTR + 4), INVALID, {"append", "select"}),
+    (dict(new_stride=248), INVALID, {"append"}), (dict(new_stride=260), INVALID, {"append"}),
+    (dict(new_stride=1 << 31), UNSUPPORTED, {"append"}), (dict(tokens=-1), INVALID, {"append"}),
+    (dict(slots=None), INVALID, {"append", "tables"}),
+    (dict(free_cap=-1), INVALID, {"tables"}), (dict(slot_cap=-1), INVALID, {"tables"}),
+])
+def test_arguments_refused(lib, kw, code, who):
+    for name, rc in _calls(lib, _shape(), **kw):
+        if name in who:
+            assert rc == code, name
+
+
+def test_null_shape(lib):
+    assert all(rc == INVALID for _, rc in _calls(lib, None))
+    assert lib.hylra_paged_workspace_bytes(None, None) == INVALID
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3)])
+def test_layouts_accepted(lib, order):
+    """Any order of the dimensions passes the pool check (the next refusal is the workspace's)."""
+    shape = (10, 2, 16, 128)
+    t = torch.empty([shape[i] for i in order], dtype=torch.bfloat16)
+    t = t.permute([order.index(i) for i in range(4)])
+    s = _shape(pool=t)
+    codes = dict(_calls(lib, s, ws=None))
+    # without a device the call ends at the device query, past the checks of the shape
+    assert all(codes[n] != UNSUPPORTED for n in POOL)
+
+
+def test_binding_checks_tensors(lib):
+    s = _shape()
+    pool = torch.zeros(10, 2, 16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        _shape(pool=pool[..., :64])
+    with pytest.raises(ValueError):
+        _shape(pool=torch.zeros(10, 2, 128, 16, dtype=torch.bfloat16).transpose(2, 3))
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    i = torch.zeros(2, 5, dtype=torch.int32)
+    n = torch.zeros(2, dtype=torch.int32)
+    out = torch.zeros(2, 8, 128)
+    ws = torch.zeros(1 << 22, dtype=torch.uint8)
+    good = [s, q, pool, pool, i, n, out, ws]
+    bad = {1: [q.float(), q[:1], q.transpose(0, 1).contiguous().transpose(0, 1)],
+           2: [pool.half(), pool[:5], torch.zeros(10, 16, 2, 128, dtype=torch.bfloat16).transpose(1, 2)],
+           4: [i.long(), i[:, :4]], 5: [n.long(), n[:1]], 6: [out.bfloat16(), out[:, :4]],
+           7: [ws]}  # nothing may live on the CPU
+    for at, values in bad.items():
+        for v in values:
+            args = list(good)
+            args[at] = v
+            with pytest.raises(ValueError):
+                H.paged_decode(*args)
+
+
+# ------------------------------------------------------------ oracle pins
+
+
+def test_oracle_attention_is_softmax():
+    g = torch.Generator().manual_seed(0)
+    q, k, v = (torch.randn(n, 8, generator=g, dtype=torch.float64) for n in (3, 11, 11))
+    want = torch.nn.functional.scaled_dot_product_attention(q[None], k[None], v[None])[0]
+    out, lse = O.attention(q.numpy(), k.numpy(), v.numpy(), 1 / math.sqrt(8))
+    assert np.allclose(out, want.numpy(), rtol=1e-13, atol=1e-13)
+    assert np.allclose(lse, torch.logsumexp(q @ k.T / math.sqrt(8), -1).numpy(), rtol=1e-13)
+    out, lse = O.attention(q.numpy(), k.numpy()[:0], v.numpy()[:0], 1.0)
+    assert (out == 0).all() and np.isneginf(lse).all()
+
+
+def test_oracle_decode_gathers_pages_in_order():
+    rng = np.random.default_rng(0)
+    k, v = rng.normal(size=(2, 7, 4))
+    pool_k, pool_v = np.full((2, 5, 1, 3, 4), np.nan)
+    table = np.array([[4, 1, 2, 99]])
+    for j in range(3):
+        rows = min(3, 7 - 3 * j)
+        pool_k[table[0, j], 0, :rows] = k[3 * j:3 * j + rows]
+        pool_v[table[0, j], 0, :rows] = v[3 * j:3 * j + rows]
+    q = rng.normal(size=(1, 2, 4))
+    out, lse = O.decode(q, pool_k, pool_v, table, [7], 3, 0.5)
+    o, l = O.attention(q[0], k, v, 0.5)
+    assert np.allclose(out[0], o) and np.allclose(lse[0], l)
+    out, _ = O.decode(q, pool_k, pool_v, table, [7], 3, 0.5, np.array([[[2, 0]]]))
+    rows = [6, 0, 1, 2]
+    assert np.allclose(out[0], O.attention(q[0], k[rows], v[rows], 0.5)[0])
+
+
+def test_oracle_select_by_hand():
+    # one head, means 1-d in effect: logits 0, 1, 2, 3 on pages 0..3 of a five-page sequence
+    means = np.zeros((5, 1, 2))
+    means[:, 0, 0] = [0, 1, 2, 3, np.nan]
+    q = np.array([[[1.0, 0.0]]])
+    idx, scores = O.select(q, means, np.array([[0, 1, 2, 3, 4]]), [17], 4, 1.0, 4, 1, 1)
+    assert idx[0, 0].tolist() == [0, 4, 3, 2]
+    c0, s = scores[0, 0]
+    assert c0 == 1 and np.allclose(s, np.exp([1, 2, 3]) / np.exp([1, 2, 3]).sum())
+    # equal means: the lower page first; fewer pages than asked for: -1
+    idx, _ = O.select(q, np.ones((5, 1, 2)), np.array([[0, 1, 2, 3, 4]]), [20], 4, 1.0, 7, 0, 1)
+    assert idx[0, 0].tolist() == [4, 0, 1, 2, 3, -1, -1]
+
+
+def test_oracle_tables_by_hand():
+    table = [[7, -1, -1], [8, 9, -1]]
+    got = O.tables([3, 8], [3, 1], [0, 1, 2], 3, table, 4, 10, 6)
+    assert got[0].tolist() == [[7, 2, -1], [8, 9, 1]]
+    assert got[1].tolist() == [31, 8, 9, 4, -1, -1]
+    assert got[2].tolist() == [6, 9] and got[3].tolist() == [0, 3, 4] and got[4] == 1
+    assert got[5:] == (False, False, False)
+
+
+def test_oracle_append_by_hand():
+    k, v, m = np.zeros((2, 1, 2, 1)), np.zeros((2, 1, 2, 1)), np.zeros((2, 1, 1))
+    new = np.array([[[2.0]], [[4.0]], [[6.0]]])
+    O.append(k, v, m, new, -new, [2, 3, -1], 2)
+    assert k[1, 0, :, 0].tolist() == [2, 4] and v[1, 0, :, 0].tolist() == [-2, -4]
+    assert m[:, 0, 0].tolist() == [0, 3]
