@@ -19,12 +19,12 @@ using namespace hylra::paged;
 namespace {
 
 constexpr size_t kSmemMax = 232448;  // 227 KB of dynamic shared memory per CTA
-static_assert(sizeof(DecodeSmem<128>) + 1024 <= kSmemMax, "decode kernel shared memory");
-static_assert(sizeof(DecodeSmem<64>) + 1024 <= kSmemMax, "decode kernel shared memory");
+constexpr size_t kSmemSM = 233472;   // 228 KB of shared memory per SM, 1 KB of it per CTA reserved
+constexpr int kCtasPerSM = 3;        // of the decode kernel, at most
 
 struct PagedLayout {
   size_t tickets, partials, total;
-  int G;  // CTAs of the decode kernel
+  int G;  // CTAs of the decode kernel, at most
 };
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -40,7 +40,7 @@ int current_device(int* dev, int* sms) {
 // every shape.
 PagedLayout make_layout(int sms) {
   PagedLayout L{};
-  L.G = std::min(sms, MAX_GRID);
+  L.G = std::min(kCtasPerSM * sms, MAX_GRID);
   L.tickets = 256;
   L.partials = L.tickets + MAX_GRID * sizeof(uint32_t);
   L.total = L.partials + (size_t)2 * L.G * DecodeShape<128>::SLOT * sizeof(float);
@@ -69,7 +69,7 @@ int check_paged(const hylra_paged_t* s) {
     return HYLRA_ERR_UNSUPPORTED;
   if ((long long)s->num_pages * s->page_size > INT_MAX) return HYLRA_ERR_UNSUPPORTED;
   if ((long long)s->max_pages * s->page_size > HYLRA_MAX_SEQLEN) return HYLRA_ERR_UNSUPPORTED;
-  const long long units = ((long long)s->max_pages * s->page_size + UTOK - 1) / UTOK;
+  const long long units = ((long long)s->max_pages * s->page_size + 63) / 64;
   if (s->num_kv_heads > INT_MAX / HYLRA_MAX_GROUP / HYLRA_MAX_BATCH ||
       (long long)s->batch * s->num_kv_heads * units > INT_MAX / 4)
     return HYLRA_ERR_UNSUPPORTED;
@@ -105,8 +105,8 @@ int check_workspace(const void* ws, size_t bytes, const PagedLayout& L) {
 
 bool bad_ptr(const void* p, size_t a) { return !p || !aligned(p, a); }
 
-// One pool as {64 elements, rows, d / 64, heads, pages}: a box is one page of
-// one head, its 64-column halves one after the other, 128-byte swizzle.
+// One pool as {64 elements, rows, d / 64, heads, pages}: a box is one piece of a
+// page of one head, its 64-column halves one after the other, 128-byte swizzle.
 int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
   auto fn = tensor_map_encoder();
   if (!fn) return HYLRA_ERR_CUDA;
@@ -119,7 +119,9 @@ int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
   const cuuint64_t strides[4] = {bytes(s->token_stride, s->page_size), 128,
                                  bytes(s->head_stride, s->num_kv_heads),
                                  bytes(s->page_stride, s->num_pages)};
-  const cuuint32_t box[5] = {64, (cuuint32_t)s->page_size, (cuuint32_t)(s->head_dim / 64), 1, 1};
+  const int utok = s->head_dim == 128 ? DecodeShape<128>::UTOK : DecodeShape<64>::UTOK;
+  const cuuint32_t box[5] = {64, (cuuint32_t)std::min(s->page_size, utok),
+                             (cuuint32_t)(s->head_dim / 64), 1, 1};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(
       tm, s->dtype == HYLRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
@@ -136,7 +138,9 @@ int allow_smem(Kernel kernel, std::atomic<uint64_t>& done, int dev) {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return HYLRA_OK;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) !=
-      cudaSuccess)
+          cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
     return HYLRA_ERR_CUDA;
   done.fetch_or(bit, std::memory_order_release);
   return HYLRA_OK;
@@ -165,12 +169,26 @@ int launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stre
 }
 
 template <int HD, typename T, bool LIST>
-int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeParams& p, int G,
+int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& p, int sms,
                   int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_decode_kernel<HD, T, LIST>;
   if (int rc = allow_smem(kernel, done, dev)) return rc;
-  return launch(kernel, dim3(G), NTHR, sizeof(DecodeSmem<HD>) + 1024, stream, 1, tmK, tmV, p);
+  // three CTAs to an SM with two stages each; where a large batch's lengths do
+  // not fit beside them, two with three
+  int ctas = kCtasPerSM;
+  p.nst = 2;
+  auto fits = [&] {
+    return (size_t)ctas * (decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B) + 1024) <= kSmemSM;
+  };
+  if (!fits()) {
+    ctas = 2;
+    p.nst = 3;
+    if (!fits()) p.nst = 2;
+  }
+  const int G = std::min(ctas * sms, MAX_GRID);
+  return launch(kernel, dim3(G), NTHR, decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B), stream, 1,
+                tmK, tmV, p);
 }
 
 int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
@@ -214,8 +232,8 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
   if ((rc = pool_map(&tmK, K, s)) || (rc = pool_map(&tmV, V, s))) return rc;
   const bool bf = s->dtype == HYLRA_BF16;
 #define HYLRA_DECODE(HD, LIST)                                                              \
-  (bf ? launch_decode<HD, __nv_bfloat16, LIST>(tmK, tmV, p, L.G, dev, stream)              \
-      : launch_decode<HD, __half, LIST>(tmK, tmV, p, L.G, dev, stream))
+  (bf ? launch_decode<HD, __nv_bfloat16, LIST>(tmK, tmV, p, sms, dev, stream)              \
+      : launch_decode<HD, __half, LIST>(tmK, tmV, p, sms, dev, stream))
   if (s->head_dim == 128) return use_list ? HYLRA_DECODE(128, true) : HYLRA_DECODE(128, false);
   return use_list ? HYLRA_DECODE(64, true) : HYLRA_DECODE(64, false);
 #undef HYLRA_DECODE

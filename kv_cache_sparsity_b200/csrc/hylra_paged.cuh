@@ -6,7 +6,7 @@
 //     promise most attention mass; one thread-block cluster each.
 //   * paged_decode_kernel: attention of one query token over all pages of its
 //     sequence or over a list of them; persistent CTAs over a static split of
-//     all (sequence, KV head, 128 tokens) units, partial results joined by the
+//     all (sequence, KV head, run of tokens) units, partial results joined by the
 //     last CTA that finishes a head.
 //
 // Every kernel is launched as a programmatic dependent and waits for the
@@ -25,8 +25,8 @@ namespace hylra {
 namespace paged {
 
 constexpr int GRP = HYLRA_MAX_GROUP;  // q-heads per KV head, the padded MMA N
-constexpr int UTOK = 128;             // tokens per unit of work
-constexpr int MAX_GRID = 256;         // CTAs of the decode kernel
+constexpr int MAX_PAGE = 128;         // tokens per page
+constexpr int MAX_GRID = 512;         // CTAs of the decode kernel
 constexpr int MAX_B = HYLRA_MAX_BATCH;
 
 // ------------------------------------------------------------ element types
@@ -75,12 +75,14 @@ struct Elem<__half> {
 
 // ----------------------------------------------------------------- decode
 
-constexpr int NWC = 8;                   // consumer warps
+constexpr int NWC = 4;                   // consumer warps
 constexpr int NTC = NWC * 32;            // consumer threads
 constexpr int NTHR = NTC + 32;           // and one producer warp
 constexpr int BAR_ID = 1;                // named barrier of the consumers
-constexpr int PPITCH = UTOK + 8;         // 16-bit words per row of P: rows 4 banks apart
-constexpr int MAX_UPAGES = UTOK / 16;    // pages per unit at the smallest page
+constexpr int BAR_UNITS = 2;             // the running sum of units is ready
+constexpr int MAX_PIECES = 8;            // pieces per unit: 128 tokens of 16-token pages
+constexpr int MAX_STAGES = 4;
+constexpr int STAGE_BYTES = 32768;       // K and V of one unit
 
 struct DecodeParams {
   const void* q;
@@ -95,37 +97,49 @@ struct DecodeParams {
   int B, Hq, Hkv, r, k;
   int ps_log2;          // page size
   int num_pages, max_pages;
+  int nst;              // ring stages
   float scale_log2;     // softmax scale * log2(e)
   long long wait_limit;
 };
 
+// A unit is UTOK tokens of one (sequence, KV head), read as pieces of
+// min(page size, UTOK) rows; consumer warp w computes the logits of tokens
+// 16*TT*w .. and, for all of the unit's tokens, the dims 16*DT*w .. of O.
 template <int HD>
 struct DecodeShape {
-  static constexpr int STAGE = 2 * UTOK * HD * 2;          // K and V of one unit
-  static constexpr int NST = HD == 128 ? 3 : 6;            // ring stages (192 KB)
-  static constexpr int NDG = HD / 16;                      // 16-dim groups of O
-  static constexpr int NTH = NWC / NDG;                    // token halves per dim group
-  static constexpr int SLOT = GRP * HD + 2 * GRP;          // partial: O, m, Z
+  static constexpr int UTOK = STAGE_BYTES / (4 * HD);  // 64 (d = 128) or 128 (d = 64)
+  static constexpr int UTOK_LOG2 = HD == 128 ? 6 : 7;
+  static constexpr int TT = UTOK / (16 * NWC);
+  static constexpr int DT = HD / (16 * NWC);
+  static constexpr int PPITCH = UTOK + 8;   // elements per row of P: rows 4 banks apart
+  static constexpr int SLOT = GRP * HD + 2 * GRP;  // partial: O, m, Z
 };
 
-template <int HD>
+template <int HD, int SPLIT>
 struct DecodeSmem {
   using S = DecodeShape<HD>;
-  uint8_t stage[S::NST][S::STAGE];  // 1024-byte aligned (128-byte swizzle atoms)
-  uint8_t qslot[S::NST][GRP * HD * 2];
-  uint16_t P[2][3][GRP][PPITCH];    // split weights of the unit's tokens, two buffers
-  float mref[2][GRP][NWC];          // what each warp's weights are relative to
+  uint16_t P[SPLIT][GRP][S::PPITCH];  // weights of the unit's tokens, split into terms
+  float mx[GRP][NWC];                 // each warp's largest logit
   float zs[NWC][GRP];
-  float oh[S::NTH > 1 ? GRP * HD : 4];  // second token half's O at a segment end
-  int nv[S::NST][MAX_UPAGES];       // valid rows of each page of the unit
-  alignas(8) uint64_t fullK[S::NST];
-  alignas(8) uint64_t fullV[S::NST];
-  alignas(8) uint64_t empty[S::NST];
-  int prefix[MAX_B + 1];            // units before sequence b (all heads)
-  int lens[MAX_B];
+  int nv[MAX_STAGES][MAX_PIECES];     // valid rows of each piece of the unit
+  alignas(8) uint64_t fullK[MAX_STAGES];
+  alignas(8) uint64_t fullV[MAX_STAGES];
+  alignas(8) uint64_t empty[MAX_STAGES];
   int abort;
   int last[2];
+  alignas(16) uint8_t qslot[MAX_STAGES][GRP * HD * 2];  // the first nst are used
 };
+
+// Dynamic shared memory: nst stages (1024-byte aligned), DecodeSmem without the
+// query slots past nst, then the sequences' units (B + 1) and lengths (B).
+template <int HD, int SPLIT>
+__host__ __device__ constexpr size_t decode_fixed(int nst) {
+  return sizeof(DecodeSmem<HD, SPLIT>) - (size_t)(MAX_STAGES - nst) * GRP * HD * 2;
+}
+template <int HD, int SPLIT>
+__host__ __device__ constexpr size_t decode_smem(int nst, int B) {
+  return 1024 + (size_t)nst * STAGE_BYTES + decode_fixed<HD, SPLIT>(nst) + (2 * (size_t)B + 1) * 4;
+}
 
 struct Unit {
   int b, h, j, U;  // part j of the U units of (b, h)
@@ -170,90 +184,140 @@ __device__ __forceinline__ int checked_len(const int32_t* seqlens, int b, int ca
 }
 
 // O, m and Z of the contributors of one head joined by log-sum-exp, by the
-// consumer threads of the CTA that finished last.
+// consumer threads of the CTA that finished last.  scratch: the ring, whose
+// copies have all landed.
 template <int HD>
-__device__ void join_partials(const DecodeParams& p, DecodeSmem<HD>& sm, int b, int h, int first,
+__device__ void join_partials(const DecodeParams& p, uint8_t* scratch, int b, int h, int first,
                               int nc, float shift, int ct) {
   using S = DecodeShape<HD>;
-  float* w = reinterpret_cast<float*>(&sm.P[0][0][0][0]);           // [nc][GRP] weights
-  float4* red = reinterpret_cast<float4*>(w + MAX_GRID * GRP);      // [NTC]
-  static_assert(sizeof(sm.P) >= (MAX_GRID * GRP + NTC * 4) * sizeof(float), "join scratch");
+  float* w = reinterpret_cast<float*>(scratch);                // [nc][GRP] weights
+  float4* red = reinterpret_cast<float4*>(w + MAX_GRID * GRP); // [max(NTC, 8 * HD / 4)]
+  float* zj = reinterpret_cast<float*>(red + 2 * NTC);         // [GRP]
+  static_assert(MAX_GRID * GRP * 4 + 2 * NTC * 16 + GRP * 4 <= STAGE_BYTES &&
+                    GRP * HD / 4 <= 2 * NTC,
+                "join scratch");
   const int cw = ct >> 5, lane = ct & 31, r = p.r;
   // contributor c of the head: its first unit's CTA left slot 2c + 1, the others slot 2c
   auto slot = [&](int c) {
     return p.partials + (size_t)(2 * (first + c) + (c == 0 ? 1 : 0)) * S::SLOT;
   };
-  if (cw < r) {  // warp g: weights of head g
-    float m = -INFINITY;
-    for (int c = lane; c < nc; c += 32) m = fmaxf(m, __ldcg(slot(c) + GRP * HD + cw));
+  // Each thread adds up float4 columns of the rows; with few columns several
+  // threads share a column's contributors.  The first loads go out before the
+  // weights are known.
+  const int ncol = r * (HD / 4);
+  const int groups = ncol >= NTC ? 1 : NTC / ncol;
+  const int part = groups > 1 ? ct / ncol : 0;
+  const int col0 = groups == 1 ? ct : part < groups ? ct - part * ncol : ncol;
+  constexpr int CB = 8;  // contributors per batch of loads
+  float4 v[CB];
+  auto load = [&](int col, int c0) {
+    const int g = col / (HD / 4), d4 = col % (HD / 4);
+#pragma unroll
+    for (int u = 0; u < CB; ++u)
+      v[u] = __ldcg(reinterpret_cast<const float4*>(slot(min(c0 + u * groups, nc - 1)) + g * HD +
+                                                    4 * d4));
+  };
+  if (col0 < ncol) load(col0, part);
+  for (int g = cw; g < r; g += NWC) {
+    constexpr int KEEP = 4;  // contributors whose m and Z a lane keeps in registers
+    float mk[KEEP], zk[KEEP], m = -INFINITY, z = 0.f;
+#pragma unroll
+    for (int t = 0; t < KEEP; ++t) {
+      const int c = lane + 32 * t;
+      mk[t] = -INFINITY;
+      zk[t] = 0.f;
+      if (c < nc) {
+        mk[t] = __ldcg(slot(c) + GRP * HD + g);
+        zk[t] = __ldcg(slot(c) + GRP * HD + GRP + g);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < KEEP; ++t) m = fmaxf(m, mk[t]);
+    for (int c = lane + 32 * KEEP; c < nc; c += 32)
+      m = fmaxf(m, __ldcg(slot(c) + GRP * HD + g));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float z = 0.f;
-    for (int c = lane; c < nc; c += 32) {
-      const float f =
-          m == -INFINITY ? 0.f : ex2_approx(__ldcg(slot(c) + GRP * HD + cw) - m);
-      w[c * GRP + cw] = f;
-      z += f * __ldcg(slot(c) + GRP * HD + GRP + cw);
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int t = 0; t < KEEP; ++t) {
+      const float f = ex2_approx(mk[t] - ms);
+      if (lane + 32 * t < nc) w[(lane + 32 * t) * GRP + g] = f;
+      z = fmaf(f, zk[t], z);
+    }
+    for (int c = lane + 32 * KEEP; c < nc; c += 32) {
+      const float f = ex2_approx(__ldcg(slot(c) + GRP * HD + g) - ms);
+      w[c * GRP + g] = f;
+      z = fmaf(f, __ldcg(slot(c) + GRP * HD + GRP + g), z);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
     if (lane == 0) {
-      sm.zs[0][cw] = z;
+      zj[g] = z;
       if (p.lse)
-        p.lse[(size_t)b * p.Hq + (size_t)h * r + cw] =
+        p.lse[(size_t)b * p.Hq + (size_t)h * r + g] =
             z == 0.f ? -INFINITY : (m + (log2f(z) - shift)) * 0.69314718f;
     }
   }
   named_bar_sync(BAR_ID, NTC);
-  const int ncol = r * (HD / 4);
-  const int groups = NTC / ncol;  // >= 1: ncol <= 256
-  const int q = ct / ncol, col = ct - q * ncol;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (q < groups) {
+  for (int col = col0; col < ncol; col += NTC) {
     const int g = col / (HD / 4), d4 = col % (HD / 4);
-#pragma unroll 4
-    for (int c = q; c < nc; c += groups) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(c) + g * HD + 4 * d4));
-      const float f = w[c * GRP + g];
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
+    if (col != col0) load(col, part);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = part;;) {
+#pragma unroll
+      for (int u = 0; u < CB; ++u) {
+        const int c = c0 + u * groups;
+        const float f = c < nc ? w[c * GRP + g] : 0.f;
+        acc.x = fmaf(v[u].x, f, acc.x);
+        acc.y = fmaf(v[u].y, f, acc.y);
+        acc.z = fmaf(v[u].z, f, acc.z);
+        acc.w = fmaf(v[u].w, f, acc.w);
+      }
+      c0 += groups * CB;
+      if (c0 >= nc) break;
+      load(col, c0);
     }
+    red[col + part * ncol] = acc;
   }
-  red[ct] = acc;
-  named_bar_sync(BAR_ID, NTC);
-  if (q == 0) {
-    const int g = col / (HD / 4), d4 = col % (HD / 4);
-    for (int o = 1; o < groups; ++o) {
-      const float4 v = red[o * ncol + col];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
+  if (groups > 1) named_bar_sync(BAR_ID, NTC);
+  if (part == 0) {
+    for (int col = col0; col < ncol; col += NTC) {
+      const int g = col / (HD / 4), d4 = col % (HD / 4);
+      float4 acc = red[col];
+      for (int o = 1; o < groups; ++o) {
+        const float4 x = red[col + o * ncol];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+      }
+      const float rz = zj[g] == 0.f ? 0.f : 1.f / zj[g];
+      *reinterpret_cast<float4*>(p.out + ((size_t)b * p.Hq + (size_t)h * r + g) * HD + 4 * d4) =
+          make_float4(acc.x * rz, acc.y * rz, acc.z * rz, acc.w * rz);
     }
-    const float z = sm.zs[0][g], rz = z == 0.f ? 0.f : 1.f / z;
-    float4* dst = reinterpret_cast<float4*>(
-        p.out + ((size_t)b * p.Hq + (size_t)h * r + g) * HD + 4 * d4);
-    *dst = make_float4(acc.x * rz, acc.y * rz, acc.z * rz, acc.w * rz);
   }
   named_bar_sync(BAR_ID, NTC);  // the scratch may be used again
 }
 
 template <int HD, typename T, bool LIST>
-__global__ void __launch_bounds__(NTHR, 1)
+__global__ void __launch_bounds__(NTHR, 3)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ DecodeParams p) {
   using S = DecodeShape<HD>;
   using E = Elem<T>;
-  constexpr int NST = S::NST;
+  using Smem = DecodeSmem<HD, E::SPLIT>;
+  constexpr int UTOK = S::UTOK, TT = S::TT, DT = S::DT, HALF = STAGE_BYTES / 2;
   extern __shared__ uint8_t smem_raw[];
-  DecodeSmem<HD>& sm = *reinterpret_cast<DecodeSmem<HD>*>(
+  uint8_t* ring = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int nst = p.nst;
+  Smem& sm = *reinterpret_cast<Smem*>(ring + nst * STAGE_BYTES);
+  int* prefix = reinterpret_cast<int*>(ring + nst * STAGE_BYTES + decode_fixed<HD, E::SPLIT>(nst));
+  int* lens = prefix + p.B + 1;  // prefix[b]: units before sequence b, of all heads
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
+  if (tid == NTHR - 1) {
+    for (int s = 0; s < nst; ++s) {
       mbar_init(&sm.fullK[s], 1);
       mbar_init(&sm.fullV[s], 1);
       mbar_init(&sm.empty[s], NWC);
@@ -261,72 +325,76 @@ __global__ void __launch_bounds__(NTHR, 1)
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (tid == 32) {
+  if (tid == 0) {
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  for (int i = tid; i < NST * MAX_UPAGES; i += NTHR) (&sm.nv[0][0])[i] = 0;
+  if (tid < MAX_STAGES * MAX_PIECES) (&sm.nv[0][0])[tid] = 0;
+  const int psl = p.ps_log2, ps = 1 << psl;
   griddep_wait();
   griddep_launch_dependents();
 
-  // units of each sequence, then their running sum
-  const int psl = p.ps_log2, ps = 1 << psl;
   for (int b = tid; b < p.B; b += NTHR) {
     const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, blockIdx.x == 0);
     const int nb = (n + ps - 1) >> psl;
     const int tokens = LIST ? min(p.k, nb) << psl : n;
-    sm.lens[b] = n;
-    sm.prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
+    lens[b] = n;
+    prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
   }
   __syncthreads();
+  // the producer warp sums the units up and goes ahead; the others follow
   if (warp == 0) {
-    const int per = (p.B + 31) / 32;
-    const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += sm.prefix[b + 1];
-    int incl = sum;
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
+      }
+      v += carry;
+      if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
     }
-    int run = incl - sum;
-    for (int b = b0; b < b1; ++b) {
-      run += sm.prefix[b + 1];
-      sm.prefix[b + 1] = run;
-    }
-    if (lane == 0) sm.prefix[0] = 0;
+    if (lane == 0) prefix[0] = 0;
+    __threadfence_block();
+    __syncwarp();
+    named_bar_arrive(BAR_UNITS, NTHR);
+  } else {
+    named_bar_sync(BAR_UNITS, NTHR);
   }
-  __syncthreads();
-  const int total = sm.prefix[p.B];
+  const int total = prefix[p.B];
   const int G = total > 0 ? min((int)gridDim.x, total) : 1;
   const bool works = (int)blockIdx.x < G && total > 0;
   const int lo = works ? (int)((long long)blockIdx.x * total / G) : 0;
   const int hi = works ? (int)((long long)(blockIdx.x + 1) * total / G) : 0;
   const int n = hi - lo;
   volatile int* abort_flag = &sm.abort;
+  const int brl = min(psl, S::UTOK_LOG2);  // rows of a piece
+  const int ppl = S::UTOK_LOG2 - brl;      // pieces of a unit
+  const uint32_t piece_bytes = (uint32_t)(HD * 2) << brl;
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     if (n == 0) return;
     const uint64_t pol = l2_evict_first_policy();
-    const int ppl = 7 - psl, ppu = 1 << ppl;  // pages per unit
-    const int UB = 32 >> ppl;                 // units whose pages one warp-wide fetch covers
-    const uint32_t page_bytes = (uint32_t)(ps * HD * 2);
+    const int ppu = 1 << ppl;
+    const int UB = 32 >> ppl;  // units whose pieces one warp-wide fetch covers
     const uint32_t qbytes = (uint32_t)(p.r * HD * 2);
     const uint8_t* qbase = static_cast<const uint8_t*>(p.q);
-    // lane l: page l % ppu of unit base + l / ppu
-    int f_page, f_rows, f_b, f_h, f_start;
+    // lane l: piece l % ppu of unit base + l / ppu
+    int f_page, f_row, f_rows, f_b, f_h, f_start;
     auto fetch = [&](int base) {
-      f_page = f_rows = f_b = f_h = f_start = 0;
+      f_page = f_row = f_rows = f_b = f_h = f_start = 0;
       const int ui = base + (lane >> ppl);
       if (ui >= n) return;
-      const Unit x = locate(sm.prefix, p.B, p.Hkv, lo + ui);
+      const Unit x = locate(prefix, p.B, p.Hkv, lo + ui);
       f_b = x.b;
       f_h = x.h;
       f_start = ui == 0 || x.j == 0;
-      const int len = sm.lens[x.b], nb = (len + ps - 1) >> psl;
-      const int e = (x.j << ppl) + (lane & (ppu - 1));
+      const int len = lens[x.b], nb = (len + ps - 1) >> psl;
+      const int first = ((x.j << ppl) + (lane & (ppu - 1))) << brl;  // token (or list) place
+      const int e = first >> psl;
       if (e >= (LIST ? min(p.k, nb) : nb)) return;
       int j = e;
       if (LIST) {
@@ -342,17 +410,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         return;
       }
       f_page = pg;
-      f_rows = min(ps, len - (j << psl));
+      f_row = first & (ps - 1);
+      f_rows = max(0, min(1 << brl, len - (j << psl) - f_row));
     };
     fetch(0);
     int issued = 0;  // units 0 .. issued-1 have started their stage's phase
+    int s = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (int base = 0; base < n && ok; base += UB) {
-      const int page = f_page, rows = f_rows, ub = f_b, uh = f_h, ust = f_start;
+      const int page = f_page, row = f_row, rows = f_rows, ub = f_b, uh = f_h, ust = f_start;
       const int cnt = min(UB, n - base);
       for (int k = 0; k < cnt; ++k) {
-        const int i = base + k, s = i % NST;
-        const uint32_t ph = (uint32_t)((i / NST) & 1);
         // after a failed wait nothing more is issued: the consumers no longer
         // wait for stages, so a refill could land in a stage still being read
         ok = mbar_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, p.wait_limit);
@@ -361,14 +430,15 @@ __global__ void __launch_bounds__(NTHR, 1)
         const int src = (k << ppl) + (lane & (ppu - 1));
         const int pg = __shfl_sync(0xffffffffu, page, src);
         const int rw = __shfl_sync(0xffffffffu, rows, src);
+        const int r0 = __shfl_sync(0xffffffffu, row, src);
         const int b = __shfl_sync(0xffffffffu, ub, k << ppl);
         const int h = __shfl_sync(0xffffffffu, uh, k << ppl);
         const int start = __shfl_sync(0xffffffffu, ust, k << ppl);
         const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rw > 0));
-        if (lane < MAX_UPAGES) sm.nv[s][lane] = lane < ppu ? rw : 0;
+        if (lane < MAX_PIECES) sm.nv[s][lane] = lane < ppu ? rw : 0;
         __syncwarp();
         if (lane == 0) {
-          const uint32_t bytes = np * page_bytes, bytesK = bytes + (start ? qbytes : 0u);
+          const uint32_t bytes = np * piece_bytes, bytesK = bytes + (start ? qbytes : 0u);
           if (bytesK) mbar_arrive_expect_tx(&sm.fullK[s], bytesK); else mbar_arrive(&sm.fullK[s]);
           if (bytes) mbar_arrive_expect_tx(&sm.fullV[s], bytes); else mbar_arrive(&sm.fullV[s]);
           if (start)
@@ -376,21 +446,24 @@ __global__ void __launch_bounds__(NTHR, 1)
                       &sm.fullK[s]);
         }
         __syncwarp();
-        const int at = lane & 15;  // lanes 0..15 the K pages, 16..31 the V pages
+        const int at = lane & 15;  // lanes 0..15 the K pieces, 16..31 the V pieces
         if (at < ppu && rw > 0) {
-          uint8_t* dst = sm.stage[s] + (lane < 16 ? 0 : S::STAGE / 2) + (size_t)at * page_bytes;
-          tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, 0, 0, h, pg,
+          uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + at * piece_bytes;
+          tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, 0, h, pg,
                       lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
         }
-        issued = i + 1;
+        ++issued;
+        if (++s == nst) {
+          s = 0;
+          ph ^= 1u;
+        }
         if (k == 0) fetch(base + UB);  // while the ring is full
       }
     }
     // never exit with a copy into this CTA's shared memory in flight
-    for (int t = 0; t < NST && t < issued; ++t) {
-      const int lastu = t + (issued - 1 - t) / NST * NST;  // last unit of stage t
-      const uint32_t ph = (uint32_t)((lastu / NST) & 1);
-      if (!mbar_drain(&sm.fullK[t], ph) || !mbar_drain(&sm.fullV[t], ph)) *abort_flag = 1;
+    for (int t = 0; t < nst && t < issued; ++t) {
+      const uint32_t lp = (uint32_t)(((issued - 1 - t) / nst) & 1);  // last phase of stage t
+      if (!mbar_drain(&sm.fullK[t], lp) || !mbar_drain(&sm.fullV[t], lp)) *abort_flag = 1;
     }
     if (*abort_flag && lane == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
     return;
@@ -402,44 +475,46 @@ __global__ void __launch_bounds__(NTHR, 1)
   const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
   // sequences without units: zeros and -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (sm.prefix[b + 1] != sm.prefix[b]) continue;
+    if (prefix[b + 1] != prefix[b]) continue;
     for (int i = ct; i < p.Hq * HD; i += NTC) p.out[(size_t)b * p.Hq * HD + i] = 0.f;
     if (p.lse)
       for (int i = ct; i < p.Hq; i += NTC) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
   }
   if (n == 0) return;
 
-  const uint32_t half_bytes = (uint32_t)ps * 128u, page_bytes = (uint32_t)ps * HD * 2u;
+  const uint32_t half_bytes = 128u << brl;  // 64 columns of a piece
   auto tok_base = [&](int t) {  // offset of token t's row (t a multiple of 16) in K or V
-    return (uint32_t)(t >> psl) * page_bytes + (uint32_t)(t & (ps - 1)) * 128u;
+    return (uint32_t)(t >> brl) * piece_bytes + (uint32_t)(t & ((1 << brl) - 1)) * 128u;
   };
-  const uint32_t kofs = tok_base(cw * 16) + (uint32_t)(xr + (mi & 1) * 8) * 128u;
+  const int tw = cw * 16 * TT;  // first token of this warp
+  const uint32_t krow = (uint32_t)(xr + (mi & 1) * 8) * 128u;
   const int kchi = mi >> 1;
-  // V: this warp's 16 dims of O, all tokens or every second half of them
-  const int dg = cw % S::NDG, th = cw / S::NDG;
-  constexpr int CPW = 8 / S::NTH;  // 16-token chunks per warp
-  const int vch = 2 * dg + (mi & 1);
-  const uint32_t vsub = (uint32_t)(vch >> 3) * half_bytes + (uint32_t)(((vch & 7) ^ xr) << 4) +
-                        (uint32_t)(xr + (mi >> 1) * 8) * 128u;
+  const uint32_t vrow = (uint32_t)(xr + (mi >> 1) * 8) * 128u;
   const float sl = p.scale_log2;
+  const uint32_t pb = smem_u32(&sm.P[0][0][0]) + (uint32_t)xr * (S::PPITCH * 2) + (uint32_t)mi * 16u;
 
   uint32_t qf[HD / 16][2];
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
-  float m_run[2] = {-INFINITY, -INFINITY}, z_run[2] = {0.f, 0.f};
-  Unit x = locate(sm.prefix, p.B, p.Hkv, lo);
-  int npend = 0;
-  int pend_b[2], pend_h[2], pend_first[2], pend_nc[2];
-  bool seg_has_start = false;
+  float o[DT][4];
+  float m_run[2], z_run[2];
+  Unit x = locate(prefix, p.B, p.Hkv, lo);
+  int npend = 0, pend_bh[2], pend_first[2], pend_nc[2];
+  bool has_start = false;  // this CTA holds the segment's first unit
+  int s = 0;
+  uint32_t ph = 0;
 
   for (int i = 0; i < n; ++i) {
-    const int s = i % NST, buf = i & 1;
-    const uint32_t ph = (uint32_t)((i / NST) & 1);
     const bool seg_start = i == 0 || x.j == 0;
     const bool seg_end = i == n - 1 || x.j == x.U - 1;
+    uint8_t* stage = ring + s * STAGE_BYTES;
     mbar_wait_bounded(&sm.fullK[s], ph, abort_flag, p.wait_limit);
-    const int nvw = min(16, max(0, sm.nv[s][(cw * 16) >> psl] - ((cw * 16) & (ps - 1))));
+    int nvw[TT];  // valid tokens of each 16
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int tok = tw + 16 * t;
+      nvw[t] = min(16, max(0, sm.nv[s][tok >> brl] - (tok & ((1 << brl) - 1))));
+    }
     if (seg_start) {
-      seg_has_start = x.j == 0;
+      has_start = x.j == 0;
       const uint32_t* qs = reinterpret_cast<const uint32_t*>(sm.qslot[s]);
 #pragma unroll
       for (int kt = 0; kt < HD / 16; ++kt) {
@@ -447,15 +522,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         qf[kt][1] = g4 < p.r ? qs[(g4 * HD + kt * 16 + 8 + 2 * c4) >> 1] : 0u;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = 0.f;
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
       m_run[0] = m_run[1] = -INFINITY;
       z_run[0] = z_run[1] = 0.f;
     }
-    // S^T = K Q^T for this warp's 16 tokens (raw logits; e & 2: token g4 + 8)
-    float a[4];
-    {
+    // S^T = K Q^T for this warp's tokens (raw logits; e & 2: token g4 + 8 of 16)
+    float a[TT][4];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
       float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t kb = smem_u32(sm.stage[s]) + kofs;
+      const uint32_t kb = smem_u32(stage) + tok_base(tw + 16 * t) + krow;
 #pragma unroll
       for (int kt = 0; kt < HD / 16; ++kt) {
         const int ch = 2 * kt + kchi;
@@ -466,141 +544,125 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        a[e] = g4 + ((e & 2) ? 8 : 0) < nvw ? a0[e] + a1[e] : -INFINITY;
+        a[t][e] = g4 + ((e & 2) ? 8 : 0) < nvw[t] ? a0[e] + a1[e] : -INFINITY;
     }
-    // largest logit of the warp's tokens per head; the weights are taken
-    // relative to the running maximum or to it, whichever is larger, so that
-    // they are ready before the other warps' maxima are known
-    float mx[2] = {fmaxf(a[0], a[2]), fmaxf(a[1], a[3])};
+    // the unit's largest logit per head, over all warps
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e & 1] = fmaxf(mx[e & 1], a[t][e]);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
       mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
     }
-    float ref[2], sub[2];
+    if (g4 == 0) {
+      sm.mx[h0][cw] = mx[0];
+      sm.mx[h1][cw] = mx[1];
+    }
+    named_bar_sync(BAR_ID, NTC);  // mx is complete; every warp is done with the last unit's P
+    float m_new[2], sub[2], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      ref[e] = fmaxf(m_run[e], mx[e] * sl);
-      sub[e] = ref[e] == -INFINITY ? 0.f : ref[e];
+      const float4 u = *reinterpret_cast<const float4*>(sm.mx[e ? h1 : h0]);
+      m_new[e] = fmaxf(m_run[e], fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)) * sl);
+      sub[e] = m_new[e] == -INFINITY ? 0.f : m_new[e];  // nothing attended to yet: weights 0
     }
-    float w[4], sum[2];
+    // weights relative to the running maximum, each split into 16-bit terms
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = ex2_approx(fmaf(a[e], sl, -sub[e & 1])) * E::SCALE;
-    sum[0] = w[0] + w[2];
-    sum[1] = w[1] + w[3];
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int head = (e & 1) ? h1 : h0, tok = cw * 16 + g4 + ((e & 2) ? 8 : 0);
-      float rest = w[e];
+      for (int e = 0; e < 4; ++e) {
+        float w = ex2_approx(fmaf(a[t][e], sl, -sub[e & 1])) * E::SCALE;
+        sum[e & 1] += w;
 #pragma unroll
-      for (int t = 0; t < E::SPLIT; ++t) {
-        const uint16_t hb = E::bits(rest);
-        sm.P[buf][t][head][tok] = hb;
-        rest -= E::value(hb);
+        for (int u = 0; u < E::SPLIT; ++u) {
+          const uint16_t hb = E::bits(w);
+          sm.P[u][(e & 1) ? h1 : h0][tw + 16 * t + g4 + ((e & 2) ? 8 : 0)] = hb;
+          w -= E::value(hb);
+        }
+      }
+    if (m_new[0] != m_run[0] || m_new[1] != m_run[1]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float al = ex2_approx(m_run[e] - sub[e]);
+        z_run[e] *= al;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          o[t][e] *= al;
+          o[t][e + 2] *= al;
+        }
+        m_run[e] = m_new[e];
       }
     }
-    if (g4 == 0) {
-      sm.mref[buf][h0][cw] = ref[0];
-      sm.mref[buf][h1][cw] = ref[1];
-    }
+    z_run[0] += sum[0];
+    z_run[1] += sum[1];
     mbar_wait_bounded(&sm.fullV[s], ph, abort_flag, p.wait_limit);
-    if (nvw < 16) {
+    bool ragged = false;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) ragged |= nvw[t] < 16;
+    if (ragged) {
       // rows past the end, or of pages that were not loaded, may hold anything
       // (NaN included): zero weights need zero values
-      uint8_t* vrow = sm.stage[s] + S::STAGE / 2 + tok_base(cw * 16);
       constexpr int CH = HD / 8;  // 16-byte chunks per row
-      for (int idx = lane; idx < 16 * CH; idx += 32) {
-        const int row = idx / CH, ch = idx % CH;
-        if (row >= nvw)
-          *reinterpret_cast<uint4*>(vrow + (ch >> 3) * half_bytes + row * 128 + (ch & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        uint8_t* rows = stage + HALF + tok_base(tw + 16 * t);
+        for (int idx = lane; idx < 16 * CH; idx += 32) {
+          const int row = idx / CH, ch = idx % CH;
+          if (row >= nvw[t])
+            *reinterpret_cast<uint4*>(rows + (ch >> 3) * half_bytes + row * 128 + (ch & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
       }
       fence_proxy_async_smem();
     }
-    named_bar_sync(BAR_ID, NTC);  // P, mref and the zeroed rows of all warps
-    float m_new[2], rw[2][NWC];
+    named_bar_sync(BAR_ID, NTC);  // P and the zeroed rows of all warps
+    // O^T += V^T P^T; the matrix unit's sums cover this unit, the running ones are fp32
+    float acc[E::SPLIT][DT][4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4* src = reinterpret_cast<const float4*>(sm.mref[buf][e ? h1 : h0]);
-      const float4 u = src[0], v = src[1];
-      rw[e][0] = u.x; rw[e][1] = u.y; rw[e][2] = u.z; rw[e][3] = u.w;
-      rw[e][4] = v.x; rw[e][5] = v.y; rw[e][6] = v.z; rw[e][7] = v.w;
-      m_new[e] = m_run[e];
+    for (int u = 0; u < E::SPLIT; ++u)
 #pragma unroll
-      for (int t = 0; t < NWC; ++t) m_new[e] = fmaxf(m_new[e], rw[e][t]);
-    }
-    const bool moved =
-        __any_sync(0xffffffffu, m_new[0] != m_run[0] || m_new[1] != m_run[1]);
-    if (moved) {
+      for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // -inf - -inf only where nothing was attended to yet: all terms are 0
-        const float mn = m_new[e] == -INFINITY ? 0.f : m_new[e];
-        const float al = ex2_approx(m_run[e] - mn);
-        z_run[e] = z_run[e] * al + sum[e] * ex2_approx(ref[e] - mn);
-        o[e] *= al;
-        o[e + 2] *= al;
+        for (int e = 0; e < 4; ++e) acc[u][t][e] = 0.f;
+    const uint32_t vb = smem_u32(stage) + HALF + vrow;
 #pragma unroll
-        for (int t = 0; t < NWC; ++t) rw[e][t] = ex2_approx(rw[e][t] - mn);
-        m_run[e] = m_new[e];
-      }
-    } else {
-      z_run[0] += sum[0];
-      z_run[1] += sum[1];
-    }
-    // O^T += V^T P^T; the matrix unit's sum covers this unit, the running one is fp32
-    const uint32_t vb = smem_u32(sm.stage[s]) + S::STAGE / 2 + vsub;
-    const uint32_t pb = smem_u32(&sm.P[buf][0][0][0]) + (uint32_t)xr * (PPITCH * 2) +
-                        (uint32_t)mi * 16u;
-    float acc[E::SPLIT][4];
+    for (int c2 = 0; c2 < UTOK / 32; ++c2) {
+      uint32_t pf[E::SPLIT][4];  // 32 tokens' B fragments of each term
 #pragma unroll
-    for (int t = 0; t < E::SPLIT; ++t)
+      for (int u = 0; u < E::SPLIT; ++u)
+        ldsm_x4(pb + (uint32_t)u * (GRP * S::PPITCH * 2) + (uint32_t)c2 * 64u, pf[u][0], pf[u][1],
+                pf[u][2], pf[u][3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int c2 = 0; c2 < CPW / 2; ++c2) {
-      uint32_t pf[E::SPLIT][4];  // two chunks' B fragments of each term
+        for (int t = 0; t < DT; ++t) {
+          const int ch = 2 * (cw * DT + t) + (mi & 1);
+          uint32_t vf[4];
+          ldsm_x4_trans(vb + tok_base(c2 * 32 + c * 16) + (uint32_t)(ch >> 3) * half_bytes +
+                            (uint32_t)(((ch & 7) ^ xr) << 4),
+                        vf[0], vf[1], vf[2], vf[3]);
 #pragma unroll
-      for (int t = 0; t < E::SPLIT; ++t)
-        ldsm_x4(pb + (uint32_t)t * (GRP * PPITCH * 2) + (uint32_t)(th * CPW + 2 * c2) * 32u,
-                pf[t][0], pf[t][1], pf[t][2], pf[t][3]);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int ch = th * CPW + 2 * c2 + u;
-        uint32_t vf[4];
-        ldsm_x4_trans(vb + tok_base(ch * 16), vf[0], vf[1], vf[2], vf[3]);
-#pragma unroll
-        for (int t = 0; t < E::SPLIT; ++t) E::mma(acc[t], vf, pf[t][2 * u], pf[t][2 * u + 1]);
-        if (moved) {  // each warp's weights are relative to their own maximum
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = 0.f;
-#pragma unroll
-            for (int t = E::SPLIT - 1; t >= 0; --t) {
-              v += acc[t][e];
-              acc[t][e] = 0.f;
-            }
-            // chunk ch was weighted by consumer warp ch
-            float f = 0.f;
-#pragma unroll
-            for (int t = 0; t < NWC; ++t) f = t == ch ? rw[e & 1][t] : f;
-            o[e] = fmaf(v, f, o[e]);
-          }
+          for (int u = 0; u < E::SPLIT; ++u) E::mma(acc[u][t], vf, pf[u][2 * c], pf[u][2 * c + 1]);
         }
-      }
     }
-    if (!moved) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[s]);
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float v = 0.f;
 #pragma unroll
-        for (int t = E::SPLIT - 1; t >= 0; --t) v += acc[t][e];
-        o[e] += v;
+        for (int u = E::SPLIT - 1; u >= 0; --u) v += acc[u][t][e];
+        o[t][e] += v;
       }
+    if (++s == nst) {
+      s = 0;
+      ph ^= 1u;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.empty[s]);
 
     if (seg_end) {
       // the lanes of a head hold parts of its Z; the warps' parts meet in zs
@@ -613,83 +675,71 @@ __global__ void __launch_bounds__(NTHR, 1)
         sm.zs[cw][h0] = z_run[0];
         sm.zs[cw][h1] = z_run[1];
       }
-      const int d0 = dg * 16 + g4;
-      if (S::NTH > 1 && th == 1) {
-        sm.oh[h0 * HD + d0] = o[0];
-        sm.oh[h1 * HD + d0] = o[1];
-        sm.oh[h0 * HD + d0 + 8] = o[2];
-        sm.oh[h1 * HD + d0 + 8] = o[3];
-      }
       named_bar_sync(BAR_ID, NTC);
-      if (th == 0) {
-        if (S::NTH > 1) {
-          o[0] += sm.oh[h0 * HD + d0];
-          o[1] += sm.oh[h1 * HD + d0];
-          o[2] += sm.oh[h0 * HD + d0 + 8];
-          o[3] += sm.oh[h1 * HD + d0 + 8];
-        }
-        float z[2] = {0.f, 0.f};
+      const bool whole = has_start && x.j == x.U - 1;
 #pragma unroll
-        for (int t = 0; t < NWC; ++t) {
-          z[0] += sm.zs[t][h0];
-          z[1] += sm.zs[t][h1];
-        }
-        const bool whole = seg_has_start && x.j == x.U - 1;
+      for (int e = 0; e < 2; ++e) {
+        const int head = e ? h1 : h0;
+        float z = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int head = e ? h1 : h0;
-          if (whole) {
-            if (head >= p.r) continue;
-            const float rz = z[e] == 0.f ? 0.f : 1.f / z[e];
-            const size_t row = (size_t)x.b * p.Hq + (size_t)x.h * p.r + head;
-            p.out[row * HD + d0] = o[e] * rz;
-            p.out[row * HD + d0 + 8] = o[e + 2] * rz;
-            if (p.lse && dg == 0 && g4 == 0)
-              p.lse[row] = z[e] == 0.f ? -INFINITY
-                                       : (m_run[e] + (log2f(z[e]) - E::SHIFT)) * 0.69314718f;
-          } else {
-            float* slot = p.partials +
-                          (size_t)(2 * (int)blockIdx.x + (seg_has_start ? 1 : 0)) * S::SLOT;
-            slot[head * HD + d0] = o[e];
-            slot[head * HD + d0 + 8] = o[e + 2];
-            if (dg == 0 && g4 == 0) {
-              slot[GRP * HD + head] = m_run[e];
-              slot[GRP * HD + GRP + head] = z[e];
-            }
+        for (int t = 0; t < NWC; ++t) z += sm.zs[t][head];
+        if (head >= p.r) continue;
+        const bool stats = cw == 0 && g4 == 0;
+        const size_t row = (size_t)x.b * p.Hq + (size_t)x.h * p.r + head;
+        float* dst = p.out + row * HD;
+        float f = z == 0.f ? 0.f : 1.f / z;
+        if (whole) {
+          if (p.lse && stats)
+            p.lse[row] = z == 0.f ? -INFINITY
+                                  : (m_run[e] + (log2f(z) - E::SHIFT)) * 0.69314718f;
+        } else {
+          float* slot = p.partials + (size_t)(2 * (int)blockIdx.x + (has_start ? 1 : 0)) * S::SLOT;
+          if (stats) {
+            slot[GRP * HD + head] = m_run[e];
+            slot[GRP * HD + GRP + head] = z;
           }
+          dst = slot + head * HD;
+          f = 1.f;
+        }
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          const int d0 = (cw * DT + t) * 16 + g4;
+          dst[d0] = o[t][e] * f;
+          dst[d0 + 8] = o[t][e + 2] * f;
         }
       }
-      if (!(seg_has_start && x.j == x.U - 1)) {
+      if (!whole) {
         // at most two a CTA: one that began before it, one that ends after it
-        const int start = sm.prefix[x.b] + x.h * x.U;
+        const int start = prefix[x.b] + x.h * x.U;
         const int cf = unit_owner(start, total, G);
-        pend_b[npend] = x.b;
-        pend_h[npend] = x.h;
+        pend_bh[npend] = x.b * p.Hkv + x.h;
         pend_first[npend] = cf;
         pend_nc[npend] = unit_owner((long long)start + x.U - 1, total, G) - cf + 1;
         ++npend;
       }
     }
-    advance(sm.prefix, p.B, p.Hkv, x);
+    advance(prefix, p.B, p.Hkv, x);
   }
   if (npend) {
     // tickets: the CTA that brings a head's count to its contributors joins it.
-    // A head's ticket is that of the CTA that holds its first unit.
-    __threadfence();
+    // A head's ticket is that of the CTA that holds its first unit.  The
+    // barriers order the other threads' stores before the ticket's release and
+    // its acquire before their loads.
     named_bar_sync(BAR_ID, NTC);
-    if (ct == 0) {
-      for (int e = 0; e < npend; ++e) {
-        uint32_t* tk = p.tickets + pend_first[e];
-        const bool last = atomic_add_acq_rel_gpu(tk, 1u) == (uint32_t)pend_nc[e] - 1u;
-        if (last) *tk = 0u;  // ready for the next call
-        sm.last[e] = last;
-      }
-      __threadfence();
+    if (ct < npend) {
+      const int e = ct;
+      uint32_t* tk = p.tickets + (e ? pend_first[1] : pend_first[0]);
+      const uint32_t nc = (uint32_t)(e ? pend_nc[1] : pend_nc[0]);
+      const bool last = atomic_add_acq_rel_gpu(tk, 1u) == nc - 1u;
+      if (last) *tk = 0u;  // ready for the next call
+      sm.last[e] = last;
     }
     named_bar_sync(BAR_ID, NTC);
-    for (int e = 0; e < npend; ++e)
-      if (sm.last[e])
-        join_partials<HD>(p, sm, pend_b[e], pend_h[e], pend_first[e], pend_nc[e], E::SHIFT, ct);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (e < npend && sm.last[e])
+        join_partials<HD>(p, ring, pend_bh[e] / p.Hkv, pend_bh[e] % p.Hkv, pend_first[e],
+                          pend_nc[e], E::SHIFT, ct);
   }
   if (*abort_flag && ct == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
 }
@@ -1044,7 +1094,7 @@ __global__ void __launch_bounds__(NT_APP)
   constexpr int RP = NT_APP / VPR;     // rows at a time
   __shared__ int slot_s[TILE_APP];
   __shared__ float part[NT_APP][9];    // 9: threads of a column land in different banks
-  __shared__ bool fresh[UTOK];         // rows of a full page that this call brings
+  __shared__ bool fresh[MAX_PAGE];         // rows of a full page that this call brings
   const int tid = threadIdx.x, v = tid % VPR, rl = tid / VPR;
   const int h = (int)blockIdx.y, t0 = (int)blockIdx.x * p.tile;
   const int cnt = min(p.tile, p.tokens - t0);

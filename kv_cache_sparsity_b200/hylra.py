@@ -385,14 +385,9 @@ def paged_workspace_bytes(shape: PagedShape) -> int:
     return n.value
 
 
-def _type_of(shape: PagedShape):
-    import torch
-    return torch.bfloat16 if shape.dtype == BF16 else torch.float16
-
-
 def _want(what, t, dtype, shape, dev, dense=True):
     """Raise unless t is a tensor of this type and shape on device index dev (contiguous if dense)."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
     if t.get_device() != dev:
         raise ValueError(f"{what}: on {t.device}, expected cuda:{dev}")
@@ -400,31 +395,60 @@ def _want(what, t, dtype, shape, dev, dense=True):
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _want_pools(s: PagedShape, K, V, dev):
+# A decode step makes a handful of these calls per layer, and a small one costs
+# the GPU less than its checks cost the host: each call tests all its tensors in
+# one expression and looks for the one to name only when that fails.
+
+
+def _want_pools(s: PagedShape, dtype, K, V, dev):
     shape = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)
     strides = (s.page_stride, s.head_stride, s.token_stride, 1)
+    if (K.dtype is dtype and V.dtype is dtype and K.shape == shape and V.shape == shape
+            and K.stride() == strides and V.stride() == strides and K.get_device() == dev
+            and V.get_device() == dev):
+        return
     for what, t in (("K_pages", K), ("V_pages", V)):
-        _want(what, t, _type_of(s), shape, dev, dense=False)
+        _want(what, t, dtype, shape, dev, dense=False)
         # the stride of a dimension of one element has no meaning
         if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
             raise ValueError(f"{what}: strides {t.stride()} differ from the shape's {strides}")
 
 
-def _paged_call(name, ws, stream, *args):
-    """args -> the entry point, with the workspace and the stream, on the workspace's device."""
-    import torch
-    dev = ws.get_device()
+def _want_query(s: PagedShape, torch, dtype, q, block_table, seqlens, dev):
+    B, i32 = s.batch, torch.int32
+    qshape, tshape = (B, s.num_q_heads, s.head_dim), (B, s.max_pages)
+    if (q.dtype is dtype and block_table.dtype is i32 and seqlens.dtype is i32
+            and q.shape == qshape and block_table.shape == tshape and seqlens.shape == (B,)
+            and q.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
+            and q.get_device() == dev and block_table.get_device() == dev
+            and seqlens.get_device() == dev):
+        return
+    _want("q", q, dtype, qshape, dev)
+    _want("block_table", block_table, i32, tshape, dev)
+    _want("seqlens", seqlens, i32, (B,), dev)
+
+
+def _want_result(s: PagedShape, torch, out, lse, dev):
+    _want("out", out, torch.float32, (s.batch, s.num_q_heads, s.head_dim), dev)
+    if lse is not None:
+        _want("lse", lse, torch.float32, (s.batch, s.num_q_heads), dev)
+
+
+def _paged_dtype(torch, s: PagedShape):
+    return torch.bfloat16 if s.dtype == BF16 else torch.float16
+
+
+def _paged_call(torch, entry, ws, dev, stream, *args):
+    """entry(*args, workspace, stream), on the workspace's device."""
     if dev < 0 or not ws.is_contiguous():
-        raise ValueError("ws: a contiguous CUDA tensor")
-    f = getattr(load(), name)
-    nbytes = ws.numel() * ws.element_size()
-    if dev == torch.cuda.current_device():
-        rc = f(*args, ws.data_ptr(), nbytes, _stream(stream))
-    else:
+        raise ValueError("ws: must be a contiguous CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            rc = f(*args, ws.data_ptr(), nbytes, _stream(stream))
+            return _paged_call(torch, entry, ws, dev, stream, *args)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    rc = entry(*args, ws.data_ptr(), ws.nbytes, st)
     if rc:
-        raise HylraError(rc, name)
+        raise HylraError(rc, entry.__name__)
 
 
 def paged_tables(shape: PagedShape, cached_lens, new_lens, free_pages, free_count, block_table,
@@ -432,18 +456,20 @@ def paged_tables(shape: PagedShape, cached_lens, new_lens, free_pages, free_coun
     """Pages, slots and lengths of a step's new tokens (all int32)."""
     import torch
     dev, B, i32 = ws.get_device(), shape.batch, torch.int32
-    for what, t, n in (("cached_lens", cached_lens, B), ("new_lens", new_lens, B),
-                       ("free_count", free_count, 1), ("seqlens_out", seqlens_out, B),
-                       ("cu_new", cu_new, B + 1), ("free_count_out", free_count_out, 1),
-                       ("free_pages", free_pages, free_pages.numel()),
-                       ("slot_map", slot_map, slot_map.numel())):
-        _want(what, t, i32, (n,), dev)
-    _want("block_table", block_table, i32, (B, shape.max_pages), dev)
-    _paged_call("hylra_paged_tables", ws, stream, ctypes.byref(shape), cached_lens.data_ptr(),
-                new_lens.data_ptr(), free_pages.data_ptr(), free_pages.numel(),
+    nfree, nslots = free_pages.numel(), slot_map.numel()
+    one = (("cached_lens", cached_lens, B), ("new_lens", new_lens, B),
+           ("free_pages", free_pages, nfree), ("free_count", free_count, 1),
+           ("seqlens_out", seqlens_out, B), ("cu_new", cu_new, B + 1),
+           ("slot_map", slot_map, nslots), ("free_count_out", free_count_out, 1),
+           ("block_table", block_table, B * shape.max_pages))
+    for what, t, n in one:
+        if not (t.dtype is i32 and t.numel() == n and t.is_contiguous()
+                and t.get_device() == dev):
+            _want(what, t, i32, (B, shape.max_pages) if t is block_table else (n,), dev)
+    _paged_call(torch, (_lib or load()).hylra_paged_tables, ws, dev, stream, ctypes.byref(shape),
+                cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), nfree,
                 free_count.data_ptr(), block_table.data_ptr(), seqlens_out.data_ptr(),
-                cu_new.data_ptr(), slot_map.data_ptr(), slot_map.numel(),
-                free_count_out.data_ptr())
+                cu_new.data_ptr(), slot_map.data_ptr(), nslots, free_count_out.data_ptr())
 
 
 def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, key_means, ws,
@@ -451,7 +477,7 @@ def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, ke
     """K_new / V_new [T, Hkv, d] (each token's heads adjacent, tokens at any stride) into the
     pools; key_means [num_pages, Hkv, d] or None."""
     import torch
-    dev, t = ws.get_device(), _type_of(shape)
+    dev, t = ws.get_device(), _paged_dtype(torch, shape)
     n, H, d = slot_map.numel(), shape.num_kv_heads, shape.head_dim
     _want("slot_map", slot_map, torch.int32, (n,), dev)
     for what, x in (("K_new", K_new), ("V_new", V_new)):
@@ -461,37 +487,24 @@ def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, ke
     stride = K_new.stride(0) if n > 1 else H * d
     if n > 1 and V_new.stride(0) != stride:
         raise ValueError("K_new and V_new must have the same token stride")
-    _want_pools(shape, K_pages, V_pages, dev)
+    _want_pools(shape, t, K_pages, V_pages, dev)
     if key_means is not None:
         _want("key_means", key_means, t, (shape.num_pages, H, d), dev)
-    _paged_call("hylra_paged_append", ws, stream, ctypes.byref(shape), K_new.data_ptr(),
-                V_new.data_ptr(), stride, slot_map.data_ptr(), n, K_pages.data_ptr(),
-                V_pages.data_ptr(), _ptr(key_means))
-
-
-def _want_query(s: PagedShape, q, block_table, seqlens, dev):
-    import torch
-    _want("q", q, _type_of(s), (s.batch, s.num_q_heads, s.head_dim), dev)
-    _want("block_table", block_table, torch.int32, (s.batch, s.max_pages), dev)
-    _want("seqlens", seqlens, torch.int32, (s.batch,), dev)
-
-
-def _want_result(s: PagedShape, out, lse, dev):
-    import torch
-    _want("out", out, torch.float32, (s.batch, s.num_q_heads, s.head_dim), dev)
-    if lse is not None:
-        _want("lse", lse, torch.float32, (s.batch, s.num_q_heads), dev)
+    _paged_call(torch, (_lib or load()).hylra_paged_append, ws, dev, stream, ctypes.byref(shape),
+                K_new.data_ptr(), V_new.data_ptr(), stride, slot_map.data_ptr(), n,
+                K_pages.data_ptr(), V_pages.data_ptr(), _ptr(key_means))
 
 
 def paged_decode(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, out, ws, lse=None,
                  stream=None):
     """Attention of one query token per sequence over its pages; lse: fp32 [B, Hq] or None."""
-    dev = ws.get_device()
-    _want_query(shape, q, block_table, seqlens, dev)
-    _want_pools(shape, K_pages, V_pages, dev)
-    _want_result(shape, out, lse, dev)
-    _paged_call("hylra_paged_decode", ws, stream, ctypes.byref(shape), q.data_ptr(),
-                K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+    import torch
+    dev, t = ws.get_device(), _paged_dtype(torch, shape)
+    _want_query(shape, torch, t, q, block_table, seqlens, dev)
+    _want_pools(shape, t, K_pages, V_pages, dev)
+    _want_result(shape, torch, out, lse, dev)
+    _paged_call(torch, (_lib or load()).hylra_paged_decode, ws, dev, stream, ctypes.byref(shape),
+                q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
                 seqlens.data_ptr(), out.data_ptr(), _ptr(lse))
 
 
@@ -499,25 +512,25 @@ def paged_select(shape: PagedShape, q, key_means, block_table, seqlens, page_idx
                  recent=1, stream=None):
     """The most promising pages of each (sequence, KV head) into page_idx int32 [B, Hkv, k]."""
     import torch
-    dev, k = ws.get_device(), page_idx.shape[-1]
-    _want_query(shape, q, block_table, seqlens, dev)
-    _want("key_means", key_means, _type_of(shape),
-          (shape.num_pages, shape.num_kv_heads, shape.head_dim), dev)
+    dev, t, k = ws.get_device(), _paged_dtype(torch, shape), page_idx.shape[-1]
+    _want_query(shape, torch, t, q, block_table, seqlens, dev)
+    _want("key_means", key_means, t, (shape.num_pages, shape.num_kv_heads, shape.head_dim), dev)
     _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
-    _paged_call("hylra_paged_select", ws, stream, ctypes.byref(shape), q.data_ptr(),
-                key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), k, sink, recent,
-                page_idx.data_ptr())
+    _paged_call(torch, (_lib or load()).hylra_paged_select, ws, dev, stream, ctypes.byref(shape),
+                q.data_ptr(), key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), k,
+                sink, recent, page_idx.data_ptr())
 
 
 def paged_decode_topk(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, page_idx, out,
                       ws, lse=None, stream=None):
     """paged_decode over the pages listed in page_idx int32 [B, Hkv, k]."""
     import torch
-    dev, k = ws.get_device(), page_idx.shape[-1]
-    _want_query(shape, q, block_table, seqlens, dev)
-    _want_pools(shape, K_pages, V_pages, dev)
+    dev, t, k = ws.get_device(), _paged_dtype(torch, shape), page_idx.shape[-1]
+    _want_query(shape, torch, t, q, block_table, seqlens, dev)
+    _want_pools(shape, t, K_pages, V_pages, dev)
     _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
-    _want_result(shape, out, lse, dev)
-    _paged_call("hylra_paged_decode_topk", ws, stream, ctypes.byref(shape), q.data_ptr(),
-                K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
-                seqlens.data_ptr(), page_idx.data_ptr(), k, out.data_ptr(), _ptr(lse))
+    _want_result(shape, torch, out, lse, dev)
+    _paged_call(torch, (_lib or load()).hylra_paged_decode_topk, ws, dev, stream,
+                ctypes.byref(shape), q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
+                block_table.data_ptr(), seqlens.data_ptr(), page_idx.data_ptr(), k,
+                out.data_ptr(), _ptr(lse))

@@ -117,8 +117,10 @@ def attention_tolerance(c: Cache):
     by that much, by 2^-22 (exponential) and by its split into 16-bit terms:
     at most (eps/2)^3 = 2^-24 (three bf16 terms) or (eps/2)^2 = 2^-22 (two fp16
     terms).  out = sum p v / sum p doubles the weights' part; the sums have at
-    most n additions of 2^-23 each, but run in tiles: 8 * 16 in the matrix unit,
-    then one a tile, 8 warps and 256 contributors.  The result is stored in
+    most n additions of 2^-23 each, but run in tiles: at most 8 * 16 in the
+    matrix unit, then one a tile of one CTA, 8 warps at most, and one a CTA that
+    holds part of the head: the tiles of 64 tokens or more that one CTA adds up
+    and the CTAs are together below n / 128 + 256.  The result is stored in
     fp32 (2^-24), all times the largest |v|.  lse: the same once, plus the
     logarithm's 2^-22 of a number below S + log n.
     """
