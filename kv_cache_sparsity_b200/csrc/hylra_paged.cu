@@ -23,7 +23,7 @@ constexpr size_t kSmemSM = 233472;   // 228 KB of shared memory per SM, 1 KB of 
 constexpr int kCtasPerSM = 3;        // of the decode kernel, at most
 
 struct PagedLayout {
-  size_t tickets, partials, total;
+  size_t ticket, partials, total;
   int G;  // CTAs of the decode kernel, at most
 };
 
@@ -41,8 +41,8 @@ int current_device(int* dev, int* sms) {
 PagedLayout make_layout(int sms) {
   PagedLayout L{};
   L.G = std::min(kCtasPerSM * sms, MAX_GRID);
-  L.tickets = 256;
-  L.partials = L.tickets + MAX_GRID * sizeof(uint32_t);
+  L.ticket = 128;
+  L.partials = 256;
   L.total = L.partials + (size_t)2 * L.G * DecodeShape<128>::SLOT * sizeof(float);
   return L;
 }
@@ -131,14 +131,17 @@ int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
   return r == CUDA_SUCCESS ? HYLRA_OK : HYLRA_ERR_CUDA;
 }
 
-// Opt a kernel in to the full shared memory, once per device.  `done` holds
-// one bit per device.
+// Once per device (`done` holds a bit of each): opt a kernel in to `smem` bytes
+// of dynamic shared memory, and have its SMs split their L1 in favour of shared
+// memory.  An SM changes that split only when it is idle: a small kernel that
+// runs under another split beside the decode kernel's start keeps its SM from
+// taking a third decode CTA (16 sequences of up to 128K: 627 against 787 us).
 template <typename Kernel>
-int allow_smem(Kernel kernel, std::atomic<uint64_t>& done, int dev) {
+int prepare(Kernel kernel, std::atomic<uint64_t>& done, int dev, size_t smem = 0) {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return HYLRA_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax) !=
-          cudaSuccess ||
+  if ((smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)smem) != cudaSuccess) ||
       cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared) != cudaSuccess)
     return HYLRA_ERR_CUDA;
@@ -173,7 +176,7 @@ int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& 
                   int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_decode_kernel<HD, T, LIST>;
-  if (int rc = allow_smem(kernel, done, dev)) return rc;
+  if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
   // three CTAs to an SM with two stages each; where a large batch's lengths do
   // not fit beside them, two with three
   int ctas = kCtasPerSM;
@@ -187,8 +190,18 @@ int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& 
     if (!fits()) p.nst = 2;
   }
   const int G = std::min(ctas * sms, MAX_GRID);
-  return launch(kernel, dim3(G), NTHR, decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B), stream, 1,
-                tmK, tmV, p);
+  if (int rc = launch(kernel, dim3(G), NTHR, decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B), stream,
+                      1, tmK, tmV, p))
+    return rc;
+  // fewer heads than CTAs: a CTA per head and 32 float4 columns; else a CTA per
+  // decode CTA (at most one head that it holds in part ends after it)
+  static std::atomic<uint64_t> join_done{0};
+  auto join = paged_join_kernel<HD, T, LIST>;
+  if (int rc = prepare(join, join_done, dev)) return rc;
+  const long long nbh = (long long)p.B * p.Hkv;
+  const int by_head = nbh <= G ? 1 : 0;
+  const dim3 grid(by_head ? (int)nbh : G, by_head ? (p.r * HD + 127) / 128 : 1);
+  return launch(join, grid, NT_JOIN, (size_t)(p.B + 1) * 4, stream, 1, p, G, by_head);
 }
 
 int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
@@ -214,7 +227,6 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
   p.out = out;
   p.lse = lse;
   p.status = reinterpret_cast<uint32_t*>(w);
-  p.tickets = reinterpret_cast<uint32_t*>(w + L.tickets);
   p.partials = reinterpret_cast<float*>(w + L.partials);
   p.B = s->batch;
   p.Hq = s->num_q_heads;
@@ -244,13 +256,16 @@ int launch_select(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
                   cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_select_kernel<HD, T>;
-  if (int rc = allow_smem(kernel, done, dev)) return rc;
+  if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
   return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
 }
 
 template <int HD, typename T>
-int launch_append(const AppendParams& p, int tiles, cudaStream_t stream) {
-  return launch(paged_append_kernel<HD, T>, dim3(tiles, p.Hkv), NT_APP, 0, stream, 1, p);
+int launch_append(const AppendParams& p, int tiles, int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = paged_append_kernel<HD, T>;
+  if (int rc = prepare(kernel, done, dev)) return rc;
+  return launch(kernel, dim3(tiles, p.Hkv), NT_APP, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -297,7 +312,7 @@ int hylra_paged_tables(const hylra_paged_t* shape, const int32_t* cached_lens,
   p.slots = slot_map;
   p.free_left = free_count_out;
   p.status = reinterpret_cast<uint32_t*>(w);
-  p.ticket = reinterpret_cast<uint32_t*>(w + L.tickets);
+  p.ticket = reinterpret_cast<uint32_t*>(w + L.ticket);
   p.B = shape->batch;
   p.ps_log2 = log2_of(shape->page_size);
   p.num_pages = shape->num_pages;
@@ -307,6 +322,8 @@ int hylra_paged_tables(const hylra_paged_t* shape, const int32_t* cached_lens,
   const long long per_cta = 4 * NT_TAB;
   const int ctas = (int)std::min<long long>(
       sms, std::max<long long>(1, (slot_capacity + per_cta - 1) / per_cta));
+  static std::atomic<uint64_t> done{0};
+  if ((rc = prepare(paged_tables_kernel, done, dev))) return rc;
   return launch(paged_tables_kernel, dim3(ctas), NT_TAB, 0, (cudaStream_t)stream, 1, p);
 }
 
@@ -353,10 +370,10 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
   const int tiles = (num_tokens + p.tile - 1) / p.tile;
   cudaStream_t st = (cudaStream_t)stream;
   if (shape->head_dim == 128)
-    return shape->dtype == HYLRA_BF16 ? launch_append<128, __nv_bfloat16>(p, tiles, st)
-                                      : launch_append<128, __half>(p, tiles, st);
-  return shape->dtype == HYLRA_BF16 ? launch_append<64, __nv_bfloat16>(p, tiles, st)
-                                    : launch_append<64, __half>(p, tiles, st);
+    return shape->dtype == HYLRA_BF16 ? launch_append<128, __nv_bfloat16>(p, tiles, dev, st)
+                                      : launch_append<128, __half>(p, tiles, dev, st);
+  return shape->dtype == HYLRA_BF16 ? launch_append<64, __nv_bfloat16>(p, tiles, dev, st)
+                                    : launch_append<64, __half>(p, tiles, dev, st);
 }
 
 int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,

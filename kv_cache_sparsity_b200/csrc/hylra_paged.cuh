@@ -6,11 +6,16 @@
 //     promise most attention mass; one thread-block cluster each.
 //   * paged_decode_kernel: attention of one query token over all pages of its
 //     sequence or over a list of them; persistent CTAs over a static split of
-//     all (sequence, KV head, run of tokens) units, partial results joined by the
-//     last CTA that finishes a head.
+//     all (sequence, KV head, run of tokens) units.
+//   * paged_join_kernel: joins the partial results of heads that several CTAs hold.
 //
 // Every kernel is launched as a programmatic dependent and waits for the
-// preceding kernel before its first access to global memory.
+// preceding kernel before its first access to global memory (but for the join's,
+// see there).  Only the decode kernel lets its dependent start early, which is
+// the join that is launched with it.  A decode kernel that started beside small
+// CTAs of another found its SMs' shared memory in pieces: where two of its CTAs
+// lay around a small one, the third had no room until one of them ended, and the
+// kernel took half as long again (16 sequences of up to 128K: 960 us, not 620).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -75,11 +80,12 @@ struct Elem<__half> {
 
 // ----------------------------------------------------------------- decode
 
-constexpr int NWC = 4;                   // consumer warps
-constexpr int NTC = NWC * 32;            // consumer threads
-constexpr int NTHR = NTC + 32;           // and one producer warp
-constexpr int BAR_ID = 1;                // named barrier of the consumers
-constexpr int BAR_UNITS = 2;             // the running sum of units is ready
+// Four warps, one on each sub-partition of an SM: with a fifth (a producer), three
+// CTAs of 128 registers a thread fit only while no two of them put their odd warp
+// on the same sub-partition, and beside a CTA of the join kernel some SMs took two
+// (16 sequences of up to 128K: 787 us).
+constexpr int NWC = 4;
+constexpr int NTHR = NWC * 32;
 constexpr int MAX_PIECES = 8;            // pieces per unit: 128 tokens of 16-token pages
 constexpr int MAX_STAGES = 4;
 constexpr int STAGE_BYTES = 32768;       // K and V of one unit
@@ -92,8 +98,8 @@ struct DecodeParams {
   float* out;
   float* lse;           // may be null
   uint32_t* status;
-  uint32_t* tickets;    // [MAX_GRID]
-  float* partials;      // [2 * gridDim.x][slot_floats]
+  float* partials;      // [2 * gridDim.x][SLOT]: of a head that began before the CTA, of one
+                        // that ends after it
   int B, Hq, Hkv, r, k;
   int ps_log2;          // page size
   int num_pages, max_pages;
@@ -103,8 +109,9 @@ struct DecodeParams {
 };
 
 // A unit is UTOK tokens of one (sequence, KV head), read as pieces of
-// min(page size, UTOK) rows; consumer warp w computes the logits of tokens
-// 16*TT*w .. and, for all of the unit's tokens, the dims 16*DT*w .. of O.
+// min(page size, UTOK) rows; warp w computes the logits of tokens 16*TT*w .. and,
+// for all of the unit's tokens, the dims 16*DT*w .. of O.  The warps request the
+// units in turn, each as soon as its stage is free.
 template <int HD>
 struct DecodeShape {
   static constexpr int UTOK = STAGE_BYTES / (4 * HD);  // 64 (d = 128) or 128 (d = 64)
@@ -126,7 +133,7 @@ struct DecodeSmem {
   alignas(8) uint64_t fullV[MAX_STAGES];
   alignas(8) uint64_t empty[MAX_STAGES];
   int abort;
-  int last[2];
+  int issued;                         // units requested so far
   alignas(16) uint8_t qslot[MAX_STAGES][GRP * HD * 2];  // the first nst are used
 };
 
@@ -183,124 +190,39 @@ __device__ __forceinline__ int checked_len(const int32_t* seqlens, int b, int ca
   return 0;
 }
 
-// O, m and Z of the contributors of one head joined by log-sum-exp, by the
-// consumer threads of the CTA that finished last.  scratch: the ring, whose
-// copies have all landed.
-template <int HD>
-__device__ void join_partials(const DecodeParams& p, uint8_t* scratch, int b, int h, int first,
-                              int nc, float shift, int ct) {
-  using S = DecodeShape<HD>;
-  float* w = reinterpret_cast<float*>(scratch);                // [nc][GRP] weights
-  float4* red = reinterpret_cast<float4*>(w + MAX_GRID * GRP); // [max(NTC, 8 * HD / 4)]
-  float* zj = reinterpret_cast<float*>(red + 2 * NTC);         // [GRP]
-  static_assert(MAX_GRID * GRP * 4 + 2 * NTC * 16 + GRP * 4 <= STAGE_BYTES &&
-                    GRP * HD / 4 <= 2 * NTC,
-                "join scratch");
-  const int cw = ct >> 5, lane = ct & 31, r = p.r;
-  // contributor c of the head: its first unit's CTA left slot 2c + 1, the others slot 2c
-  auto slot = [&](int c) {
-    return p.partials + (size_t)(2 * (first + c) + (c == 0 ? 1 : 0)) * S::SLOT;
-  };
-  // Each thread adds up float4 columns of the rows; with few columns several
-  // threads share a column's contributors.  The first loads go out before the
-  // weights are known.
-  const int ncol = r * (HD / 4);
-  const int groups = ncol >= NTC ? 1 : NTC / ncol;
-  const int part = groups > 1 ? ct / ncol : 0;
-  const int col0 = groups == 1 ? ct : part < groups ? ct - part * ncol : ncol;
-  constexpr int CB = 8;  // contributors per batch of loads
-  float4 v[CB];
-  auto load = [&](int col, int c0) {
-    const int g = col / (HD / 4), d4 = col % (HD / 4);
-#pragma unroll
-    for (int u = 0; u < CB; ++u)
-      v[u] = __ldcg(reinterpret_cast<const float4*>(slot(min(c0 + u * groups, nc - 1)) + g * HD +
-                                                    4 * d4));
-  };
-  if (col0 < ncol) load(col0, part);
-  for (int g = cw; g < r; g += NWC) {
-    constexpr int KEEP = 4;  // contributors whose m and Z a lane keeps in registers
-    float mk[KEEP], zk[KEEP], m = -INFINITY, z = 0.f;
-#pragma unroll
-    for (int t = 0; t < KEEP; ++t) {
-      const int c = lane + 32 * t;
-      mk[t] = -INFINITY;
-      zk[t] = 0.f;
-      if (c < nc) {
-        mk[t] = __ldcg(slot(c) + GRP * HD + g);
-        zk[t] = __ldcg(slot(c) + GRP * HD + GRP + g);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < KEEP; ++t) m = fmaxf(m, mk[t]);
-    for (int c = lane + 32 * KEEP; c < nc; c += 32)
-      m = fmaxf(m, __ldcg(slot(c) + GRP * HD + g));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int t = 0; t < KEEP; ++t) {
-      const float f = ex2_approx(mk[t] - ms);
-      if (lane + 32 * t < nc) w[(lane + 32 * t) * GRP + g] = f;
-      z = fmaf(f, zk[t], z);
-    }
-    for (int c = lane + 32 * KEEP; c < nc; c += 32) {
-      const float f = ex2_approx(__ldcg(slot(c) + GRP * HD + g) - ms);
-      w[c * GRP + g] = f;
-      z = fmaf(f, __ldcg(slot(c) + GRP * HD + GRP + g), z);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    if (lane == 0) {
-      zj[g] = z;
-      if (p.lse)
-        p.lse[(size_t)b * p.Hq + (size_t)h * r + g] =
-            z == 0.f ? -INFINITY : (m + (log2f(z) - shift)) * 0.69314718f;
-    }
+// prefix[b + 1]: units of sequence b times Hkv, by all threads; then their
+// running sum, by warp 0.
+template <bool LIST, int UTOK>
+__device__ __forceinline__ void count_units(const DecodeParams& p, int* prefix, int* lens,
+                                            bool report) {
+  const int psl = p.ps_log2;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, report);
+    const int nb = (n + (1 << psl) - 1) >> psl;
+    const int tokens = LIST ? min(p.k, nb) << psl : n;
+    if (lens) lens[b] = n;
+    prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
   }
-  named_bar_sync(BAR_ID, NTC);
-  for (int col = col0; col < ncol; col += NTC) {
-    const int g = col / (HD / 4), d4 = col % (HD / 4);
-    if (col != col0) load(col, part);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = part;;) {
+}
+__device__ __forceinline__ void sum_units(const DecodeParams& p, int* prefix) {
+  const int lane = threadIdx.x;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
 #pragma unroll
-      for (int u = 0; u < CB; ++u) {
-        const int c = c0 + u * groups;
-        const float f = c < nc ? w[c * GRP + g] : 0.f;
-        acc.x = fmaf(v[u].x, f, acc.x);
-        acc.y = fmaf(v[u].y, f, acc.y);
-        acc.z = fmaf(v[u].z, f, acc.z);
-        acc.w = fmaf(v[u].w, f, acc.w);
-      }
-      c0 += groups * CB;
-      if (c0 >= nc) break;
-      load(col, c0);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += o;
     }
-    red[col + part * ncol] = acc;
+    v += carry;
+    if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
+    carry = __shfl_sync(0xffffffffu, v, 31);
   }
-  if (groups > 1) named_bar_sync(BAR_ID, NTC);
-  if (part == 0) {
-    for (int col = col0; col < ncol; col += NTC) {
-      const int g = col / (HD / 4), d4 = col % (HD / 4);
-      float4 acc = red[col];
-      for (int o = 1; o < groups; ++o) {
-        const float4 x = red[col + o * ncol];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-      }
-      const float rz = zj[g] == 0.f ? 0.f : 1.f / zj[g];
-      *reinterpret_cast<float4*>(p.out + ((size_t)b * p.Hq + (size_t)h * r + g) * HD + 4 * d4) =
-          make_float4(acc.x * rz, acc.y * rz, acc.z * rz, acc.w * rz);
-    }
-  }
-  named_bar_sync(BAR_ID, NTC);  // the scratch may be used again
+  if (lane == 0) prefix[0] = 0;
 }
 
 template <int HD, typename T, bool LIST>
-__global__ void __launch_bounds__(NTHR, 3)
+__global__ void __launch_bounds__(NTHR, 4)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ DecodeParams p) {
@@ -323,6 +245,7 @@ __global__ void __launch_bounds__(NTHR, 3)
       mbar_init(&sm.empty[s], NWC);
     }
     sm.abort = 0;
+    sm.issued = 0;
     fence_mbar_init();
   }
   if (tid == 0) {
@@ -334,35 +257,10 @@ __global__ void __launch_bounds__(NTHR, 3)
   griddep_wait();
   griddep_launch_dependents();
 
-  for (int b = tid; b < p.B; b += NTHR) {
-    const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, blockIdx.x == 0);
-    const int nb = (n + ps - 1) >> psl;
-    const int tokens = LIST ? min(p.k, nb) << psl : n;
-    lens[b] = n;
-    prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
-  }
+  count_units<LIST, UTOK>(p, prefix, lens, blockIdx.x == 0);
   __syncthreads();
-  // the producer warp sums the units up and goes ahead; the others follow
-  if (warp == 0) {
-    int carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += o;
-      }
-      v += carry;
-      if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
-      carry = __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) prefix[0] = 0;
-    __threadfence_block();
-    __syncwarp();
-    named_bar_arrive(BAR_UNITS, NTHR);
-  } else {
-    named_bar_sync(BAR_UNITS, NTHR);
-  }
+  if (warp == 0) sum_units(p, prefix);
+  __syncthreads();
   const int total = prefix[p.B];
   const int G = total > 0 ? min((int)gridDim.x, total) : 1;
   const bool works = (int)blockIdx.x < G && total > 0;
@@ -374,114 +272,91 @@ __global__ void __launch_bounds__(NTHR, 3)
   const int ppl = S::UTOK_LOG2 - brl;      // pieces of a unit
   const uint32_t piece_bytes = (uint32_t)(HD * 2) << brl;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------- producer
-    if (n == 0) return;
-    const uint64_t pol = l2_evict_first_policy();
-    const int ppu = 1 << ppl;
-    const int UB = 32 >> ppl;  // units whose pieces one warp-wide fetch covers
-    const uint32_t qbytes = (uint32_t)(p.r * HD * 2);
-    const uint8_t* qbase = static_cast<const uint8_t*>(p.q);
-    // lane l: piece l % ppu of unit base + l / ppu
-    int f_page, f_row, f_rows, f_b, f_h, f_start;
-    auto fetch = [&](int base) {
-      f_page = f_row = f_rows = f_b = f_h = f_start = 0;
-      const int ui = base + (lane >> ppl);
-      if (ui >= n) return;
-      const Unit x = locate(prefix, p.B, p.Hkv, lo + ui);
-      f_b = x.b;
-      f_h = x.h;
-      f_start = ui == 0 || x.j == 0;
-      const int len = lens[x.b], nb = (len + ps - 1) >> psl;
-      const int first = ((x.j << ppl) + (lane & (ppu - 1))) << brl;  // token (or list) place
-      const int e = first >> psl;
-      if (e >= (LIST ? min(p.k, nb) : nb)) return;
-      int j = e;
-      if (LIST) {
-        j = __ldcg(p.list + ((size_t)x.b * p.Hkv + x.h) * p.k + e);
-        if (j < 0 || j >= nb) {
-          if (j != -1) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
-          return;
-        }
-      }
-      const int pg = __ldcg(p.table + (size_t)x.b * p.max_pages + j);
-      if (pg < 0 || pg >= p.num_pages) {
-        atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
-        return;
-      }
-      f_page = pg;
-      f_row = first & (ps - 1);
-      f_rows = max(0, min(1 << brl, len - (j << psl) - f_row));
-    };
-    fetch(0);
-    int issued = 0;  // units 0 .. issued-1 have started their stage's phase
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int base = 0; base < n && ok; base += UB) {
-      const int page = f_page, row = f_row, rows = f_rows, ub = f_b, uh = f_h, ust = f_start;
-      const int cnt = min(UB, n - base);
-      for (int k = 0; k < cnt; ++k) {
-        // after a failed wait nothing more is issued: the consumers no longer
-        // wait for stages, so a refill could land in a stage still being read
-        ok = mbar_wait_bounded(&sm.empty[s], ph ^ 1u, abort_flag, p.wait_limit);
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-        if (!ok) break;
-        const int src = (k << ppl) + (lane & (ppu - 1));
-        const int pg = __shfl_sync(0xffffffffu, page, src);
-        const int rw = __shfl_sync(0xffffffffu, rows, src);
-        const int r0 = __shfl_sync(0xffffffffu, row, src);
-        const int b = __shfl_sync(0xffffffffu, ub, k << ppl);
-        const int h = __shfl_sync(0xffffffffu, uh, k << ppl);
-        const int start = __shfl_sync(0xffffffffu, ust, k << ppl);
-        const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rw > 0));
-        if (lane < MAX_PIECES) sm.nv[s][lane] = lane < ppu ? rw : 0;
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t bytes = np * piece_bytes, bytesK = bytes + (start ? qbytes : 0u);
-          if (bytesK) mbar_arrive_expect_tx(&sm.fullK[s], bytesK); else mbar_arrive(&sm.fullK[s]);
-          if (bytes) mbar_arrive_expect_tx(&sm.fullV[s], bytes); else mbar_arrive(&sm.fullV[s]);
-          if (start)
-            bulk_load(sm.qslot[s], qbase + ((size_t)b * p.Hq + (size_t)h * p.r) * HD * 2, qbytes,
-                      &sm.fullK[s]);
-        }
-        __syncwarp();
-        const int at = lane & 15;  // lanes 0..15 the K pieces, 16..31 the V pieces
-        if (at < ppu && rw > 0) {
-          uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + at * piece_bytes;
-          tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, 0, h, pg,
-                      lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
-        }
-        ++issued;
-        if (++s == nst) {
-          s = 0;
-          ph ^= 1u;
-        }
-        if (k == 0) fetch(base + UB);  // while the ring is full
-      }
-    }
-    // never exit with a copy into this CTA's shared memory in flight
-    for (int t = 0; t < nst && t < issued; ++t) {
-      const uint32_t lp = (uint32_t)(((issued - 1 - t) / nst) & 1);  // last phase of stage t
-      if (!mbar_drain(&sm.fullK[t], lp) || !mbar_drain(&sm.fullV[t], lp)) *abort_flag = 1;
-    }
-    if (*abort_flag && lane == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
-    return;
-  }
-
-  // --------------------------------------------------------------- consumers
-  const int cw = warp - 1, ct = tid - 32;
-  const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
-  const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
+  const int cw = warp;
   // sequences without units: zeros and -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;
-    for (int i = ct; i < p.Hq * HD; i += NTC) p.out[(size_t)b * p.Hq * HD + i] = 0.f;
+    for (int i = tid; i < p.Hq * HD; i += NTHR) p.out[(size_t)b * p.Hq * HD + i] = 0.f;
     if (p.lse)
-      for (int i = ct; i < p.Hq; i += NTC) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+      for (int i = tid; i < p.Hq; i += NTHR) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
   }
   if (n == 0) return;
 
+  // Requests.  Unit i is warp i % 4's; a warp looks up the pages of its next
+  // 32 / (pieces of a unit) units at once, lane l those of piece l % ppu.
+  const uint64_t pol = l2_evict_first_policy();
+  const int ppu = 1 << ppl, UB = 32 >> ppl;
+  int f_page = 0, f_row = 0, f_rows = 0, f_b = 0, f_h = 0, f_start = 0;
+  auto fetch = [&](int base) {
+    f_rows = f_start = 0;
+    const int ui = base + NWC * (lane >> ppl);
+    if (ui >= n) return;
+    const Unit x = locate(prefix, p.B, p.Hkv, lo + ui);
+    f_b = x.b;
+    f_h = x.h;
+    f_start = ui == 0 || x.j == 0;
+    const int len = lens[x.b], nb = (len + ps - 1) >> psl;
+    const int first = ((x.j << ppl) + (lane & (ppu - 1))) << brl;  // token (or list) place
+    const int e = first >> psl;
+    if (e >= (LIST ? min(p.k, nb) : nb)) return;
+    int j = e;
+    if (LIST) {
+      j = __ldcg(p.list + ((size_t)x.b * p.Hkv + x.h) * p.k + e);
+      if (j < 0 || j >= nb) {
+        if (j != -1) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+        return;
+      }
+    }
+    const int pg = __ldcg(p.table + (size_t)x.b * p.max_pages + j);
+    if (pg < 0 || pg >= p.num_pages) {
+      atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+      return;
+    }
+    f_page = pg;
+    f_row = first & (ps - 1);
+    f_rows = max(0, min(1 << brl, len - (j << psl) - f_row));
+  };
+  auto issue = [&](int i, int s) {  // unit i (this warp's) into stage s
+    // after a failed wait nothing more is requested: the others no longer wait
+    // for stages, so a copy could land in a stage still being read
+    if (__any_sync(0xffffffffu, *abort_flag)) return;
+    const int k = (i / NWC) & (UB - 1);
+    if (k == 0) fetch(i);
+    const int src = (k << ppl) + (lane & (ppu - 1));
+    const int pg = __shfl_sync(0xffffffffu, f_page, src);
+    const int rw = __shfl_sync(0xffffffffu, f_rows, src);
+    const int r0 = __shfl_sync(0xffffffffu, f_row, src);
+    const int b = __shfl_sync(0xffffffffu, f_b, k << ppl);
+    const int h = __shfl_sync(0xffffffffu, f_h, k << ppl);
+    const int start = __shfl_sync(0xffffffffu, f_start, k << ppl);
+    const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rw > 0));
+    if (lane < MAX_PIECES) sm.nv[s][lane] = lane < ppu ? rw : 0;
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t qbytes = start ? (uint32_t)(p.r * HD * 2) : 0u;
+      const uint32_t bytes = np * piece_bytes, bytesK = bytes + qbytes;
+      sm.issued = i + 1;
+      if (bytesK) mbar_arrive_expect_tx(&sm.fullK[s], bytesK); else mbar_arrive(&sm.fullK[s]);
+      if (bytes) mbar_arrive_expect_tx(&sm.fullV[s], bytes); else mbar_arrive(&sm.fullV[s]);
+      if (start)
+        bulk_load(sm.qslot[s],
+                  static_cast<const uint8_t*>(p.q) +
+                      ((size_t)b * p.Hq + (size_t)h * p.r) * HD * 2,
+                  qbytes, &sm.fullK[s]);
+    }
+    __syncwarp();
+    const int at = lane & 15;  // lanes 0..15 the K pieces, 16..31 the V pieces
+    if (at < ppu && rw > 0) {
+      uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + at * piece_bytes;
+      tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, 0, h, pg,
+                  lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
+    }
+  };
+  for (int i = 0; i < nst && i < n; ++i)  // nst <= 4: a different warp each
+    if (i == cw) issue(i, i);
+
+  const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
+  const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
   const uint32_t half_bytes = 128u << brl;  // 64 columns of a piece
   auto tok_base = [&](int t) {  // offset of token t's row (t a multiple of 16) in K or V
     return (uint32_t)(t >> brl) * piece_bytes + (uint32_t)(t & ((1 << brl) - 1)) * 128u;
@@ -497,7 +372,6 @@ __global__ void __launch_bounds__(NTHR, 3)
   float o[DT][4];
   float m_run[2], z_run[2];
   Unit x = locate(prefix, p.B, p.Hkv, lo);
-  int npend = 0, pend_bh[2], pend_first[2], pend_nc[2];
   bool has_start = false;  // this CTA holds the segment's first unit
   int s = 0;
   uint32_t ph = 0;
@@ -561,7 +435,7 @@ __global__ void __launch_bounds__(NTHR, 3)
       sm.mx[h0][cw] = mx[0];
       sm.mx[h1][cw] = mx[1];
     }
-    named_bar_sync(BAR_ID, NTC);  // mx is complete; every warp is done with the last unit's P
+    __syncthreads();  // mx is complete; every warp is done with the last unit's P
     float m_new[2], sub[2], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -618,7 +492,7 @@ __global__ void __launch_bounds__(NTHR, 3)
       }
       fence_proxy_async_smem();
     }
-    named_bar_sync(BAR_ID, NTC);  // P and the zeroed rows of all warps
+    __syncthreads();  // P and the zeroed rows of all warps
     // O^T += V^T P^T; the matrix unit's sums cover this unit, the running ones are fp32
     float acc[E::SPLIT][DT][4];
 #pragma unroll
@@ -648,8 +522,14 @@ __global__ void __launch_bounds__(NTHR, 3)
           for (int u = 0; u < E::SPLIT; ++u) E::mma(acc[u][t], vf, pf[u][2 * c], pf[u][2 * c + 1]);
         }
     }
+    // the stage is free once all warps are here; the warp whose turn it is
+    // requests the next unit before it waits for the data of another
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
+    if (i + nst < n && ((i + nst) & (NWC - 1)) == cw) {
+      mbar_wait_bounded(&sm.empty[s], ph, abort_flag, p.wait_limit);
+      issue(i + nst, s);
+    }
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -675,7 +555,7 @@ __global__ void __launch_bounds__(NTHR, 3)
         sm.zs[cw][h0] = z_run[0];
         sm.zs[cw][h1] = z_run[1];
       }
-      named_bar_sync(BAR_ID, NTC);
+      __syncthreads();
       const bool whole = has_start && x.j == x.U - 1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -708,40 +588,137 @@ __global__ void __launch_bounds__(NTHR, 3)
           dst[d0 + 8] = o[t][e + 2] * f;
         }
       }
-      if (!whole) {
-        // at most two a CTA: one that began before it, one that ends after it
-        const int start = prefix[x.b] + x.h * x.U;
-        const int cf = unit_owner(start, total, G);
-        pend_bh[npend] = x.b * p.Hkv + x.h;
-        pend_first[npend] = cf;
-        pend_nc[npend] = unit_owner((long long)start + x.U - 1, total, G) - cf + 1;
-        ++npend;
-      }
     }
     advance(prefix, p.B, p.Hkv, x);
   }
-  if (npend) {
-    // tickets: the CTA that brings a head's count to its contributors joins it.
-    // A head's ticket is that of the CTA that holds its first unit.  The
-    // barriers order the other threads' stores before the ticket's release and
-    // its acquire before their loads.
-    named_bar_sync(BAR_ID, NTC);
-    if (ct < npend) {
-      const int e = ct;
-      uint32_t* tk = p.tickets + (e ? pend_first[1] : pend_first[0]);
-      const uint32_t nc = (uint32_t)(e ? pend_nc[1] : pend_nc[0]);
-      const bool last = atomic_add_acq_rel_gpu(tk, 1u) == nc - 1u;
-      if (last) *tk = 0u;  // ready for the next call
-      sm.last[e] = last;
+  __syncthreads();
+  if (*abort_flag && tid == 0) {
+    // never exit with a copy into this CTA's shared memory in flight
+    const int issued = sm.issued;
+    for (int t = 0; t < nst && t < issued; ++t) {
+      const uint32_t lp = (uint32_t)(((issued - 1 - t) / nst) & 1);  // last phase of stage t
+      mbar_drain(&sm.fullK[t], lp);
+      mbar_drain(&sm.fullV[t], lp);
     }
-    named_bar_sync(BAR_ID, NTC);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (e < npend && sm.last[e])
-        join_partials<HD>(p, ring, pend_bh[e] / p.Hkv, pend_bh[e] % p.Hkv, pend_first[e],
-                          pend_nc[e], E::SHIFT, ct);
+    atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
   }
-  if (*abort_flag && ct == 0) atomicOr(p.status, HYLRA_STATUS_TIMEOUT);
+}
+
+// Joins by log-sum-exp the heads whose units several CTAs hold.  Grid (heads or
+// decode CTAs, column parts): with by_head, x is a (sequence, KV head); else it
+// is a decode CTA, for the head that begins in it and ends in a later one (at
+// most one).  A warp takes every fourth contributor, a lane one float4 column;
+// all of a warp's loads of 64 contributors go out together, so that a join is
+// one trip to L2.  It replaced a join by the last CTA to finish a head (a ticket
+// each): one SM then fetched all partials, 7-8 us behind the last unit of one
+// 32K sequence, against about 2.5 us here.
+constexpr int NT_JOIN = 128;
+
+template <int HD, typename T, bool LIST>
+__global__ void __launch_bounds__(NT_JOIN)
+    paged_join_kernel(const __grid_constant__ DecodeParams p, int grid_decode, int by_head) {
+  using S = DecodeShape<HD>;
+  constexpr int NG = NT_JOIN / 32, CB = 16;
+  extern __shared__ int prefix[];  // [B + 1]
+  __shared__ float4 wacc[NG][32];
+  __shared__ float wm[NG][32], wz[NG][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = p.r;
+  // Lengths are older than the decode kernel, which has waited for everything
+  // before it: they are read ahead of the wait.
+  count_units<LIST, S::UTOK>(p, prefix, nullptr, false);
+  __syncthreads();
+  if (warp == 0) sum_units(p, prefix);
+  __syncthreads();
+  const int total = prefix[p.B], G = min(grid_decode, max(total, 1));
+  int bh = 0, first = 0, nc = 0;
+  if (by_head) {
+    bh = (int)blockIdx.x;
+    const int b = bh / p.Hkv, U = (prefix[b + 1] - prefix[b]) / p.Hkv;
+    if (U > 0) {
+      const int start = prefix[b] + (bh - b * p.Hkv) * U;
+      first = unit_owner(start, total, G);
+      nc = unit_owner((long long)start + U - 1, total, G) - first + 1;
+    }
+  } else if ((int)blockIdx.x < G && total > 0) {
+    first = (int)blockIdx.x;
+    const int lo = (int)((long long)first * total / G);
+    const int end = (int)((long long)(first + 1) * total / G) - 1;
+    const Unit x = locate(prefix, p.B, p.Hkv, end);
+    bh = x.b * p.Hkv + x.h;
+    if (end - x.j >= lo) nc = unit_owner((long long)end - x.j + x.U - 1, total, G) - first + 1;
+  }
+  griddep_wait();
+  if (nc < 2) return;
+  const int ncol = r * (HD / 4);
+  for (int col0 = (int)blockIdx.y * 32; col0 < ncol; col0 += (int)gridDim.y * 32) {
+    const int col = min(col0 + lane, ncol - 1), g = col / (HD / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, z = 0.f;
+    for (int c0 = warp; c0 < nc; c0 += NG * CB) {
+      float4 o[CB];
+      float mc[CB], zc[CB];
+#pragma unroll
+      for (int u = 0; u < CB; ++u) {
+        // past the end the last one again: loads under the same condition in all lanes
+        const int c = min(c0 + u * NG, nc - 1);
+        // contributor 0 holds the head's first unit and left slot 2c + 1, the others slot 2c
+        const float* slot = p.partials + (size_t)(2 * (first + c) + (c == 0 ? 1 : 0)) * S::SLOT;
+        mc[u] = __ldcg(slot + GRP * HD + g);
+        zc[u] = __ldcg(slot + GRP * HD + GRP + g);
+        o[u] = __ldcg(reinterpret_cast<const float4*>(slot) + col);
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < CB; ++u) mn = fmaxf(mn, mc[u]);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      const float al = ex2_approx(m - ms);
+      acc.x *= al;
+      acc.y *= al;
+      acc.z *= al;
+      acc.w *= al;
+      z *= al;
+#pragma unroll
+      for (int u = 0; u < CB; ++u) {
+        if (c0 + u * NG >= nc) break;
+        const float f = ex2_approx(mc[u] - ms);
+        z = fmaf(f, zc[u], z);
+        acc.x = fmaf(f, o[u].x, acc.x);
+        acc.y = fmaf(f, o[u].y, acc.y);
+        acc.z = fmaf(f, o[u].z, acc.z);
+        acc.w = fmaf(f, o[u].w, acc.w);
+      }
+      m = mn;
+    }
+    wacc[warp][lane] = acc;
+    wm[warp][lane] = m;
+    wz[warp][lane] = z;
+    __syncthreads();
+    if (warp == 0 && col0 + lane < ncol) {
+      float mn = m;
+#pragma unroll
+      for (int w = 1; w < NG; ++w) mn = fmaxf(mn, wm[w][lane]);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float zz = 0.f;
+#pragma unroll
+      for (int w = 0; w < NG; ++w) {
+        const float f = ex2_approx(wm[w][lane] - ms);
+        const float4 x = wacc[w][lane];
+        zz = fmaf(f, wz[w][lane], zz);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+      }
+      const size_t row = (size_t)bh * r + g;  // b * Hq + h * r + g
+      const float rz = zz == 0.f ? 0.f : 1.f / zz;
+      *reinterpret_cast<float4*>(p.out + row * HD + 4 * (col % (HD / 4))) =
+          make_float4(v.x * rz, v.y * rz, v.z * rz, v.w * rz);
+      if (p.lse && col % (HD / 4) == 0)
+        p.lse[row] = zz == 0.f ? -INFINITY : (mn + (log2f(zz) - Elem<T>::SHIFT)) * 0.69314718f;
+    }
+    __syncthreads();
+  }
 }
 
 // ----------------------------------------------------------------- select
@@ -918,7 +895,6 @@ __global__ void __launch_bounds__(NT_SEL)
   const int bh = (int)blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   cluster_arrive_relaxed();
   griddep_wait();
-  griddep_launch_dependents();
   const int psl = p.ps_log2;
   const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, h == 0 && rank == 0 && tid == 0);
   const int nb = (n + (1 << psl) - 1) >> psl;
@@ -1100,7 +1076,6 @@ __global__ void __launch_bounds__(NT_APP)
   const int cnt = min(p.tile, p.tokens - t0);
   const int ps = 1 << p.ps_log2;
   griddep_wait();
-  griddep_launch_dependents();
   for (int i = tid; i < cnt; i += NT_APP) {
     int s = __ldcg(p.slots + t0 + i);
     if (s < 0 || s >= p.num_slots) {
@@ -1221,7 +1196,6 @@ __global__ void __launch_bounds__(NT_TAB)
   const int tid = threadIdx.x, psl = p.ps_log2, ps = 1 << psl;
   const bool report = blockIdx.x == 0;
   griddep_wait();
-  griddep_launch_dependents();
   if (tid == 0) {
     int f = __ldcg(p.free_count);
     if (f < 0 || f > p.free_cap) {
