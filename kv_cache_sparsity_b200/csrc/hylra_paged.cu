@@ -190,18 +190,20 @@ int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& 
     if (!fits()) p.nst = 2;
   }
   const int G = std::min(ctas * sms, MAX_GRID);
-  if (int rc = launch(kernel, dim3(G), NTHR, decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B), stream,
-                      1, tmK, tmV, p))
-    return rc;
+  const size_t smem = decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B);
+  if (int rc = launch(kernel, dim3(G), NTHR, smem, stream, 1, tmK, tmV, p)) return rc;
   // fewer heads than CTAs: a CTA per head and 32 float4 columns; else a CTA per
   // decode CTA (at most one head that it holds in part ends after it)
   static std::atomic<uint64_t> join_done{0};
   auto join = paged_join_kernel<HD, T, LIST>;
-  if (int rc = prepare(join, join_done, dev)) return rc;
+  if (int rc = prepare(join, join_done, dev, kSmemMax - JOIN_STATIC)) return rc;
   const long long nbh = (long long)p.B * p.Hkv;
   const int by_head = nbh <= G ? 1 : 0;
-  const dim3 grid(by_head ? (int)nbh : G, by_head ? (p.r * HD + 127) / 128 : 1);
-  return launch(join, grid, NT_JOIN, (size_t)(p.B + 1) * 4, stream, 1, p, G, by_head);
+  const int parts = std::min((p.r * HD + 127) / 128, std::max(1, G / (int)std::max(1LL, nbh)));
+  const dim3 grid(by_head ? (int)nbh : G, by_head ? parts : 1);
+  // its CTAs ask for as much shared memory as the decode kernel's, so that those
+  // of the next call find its SMs in pieces that fit (see paged_join_kernel)
+  return launch(join, grid, NT_JOIN, smem - JOIN_STATIC, stream, 1, p, G, by_head);
 }
 
 int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,

@@ -612,17 +612,20 @@ __global__ void __launch_bounds__(NTHR, 4)
 // one trip to L2.  It replaced a join by the last CTA to finish a head (a ticket
 // each): one SM then fetched all partials, 7-8 us behind the last unit of one
 // 32K sequence, against about 2.5 us here.
-constexpr int NT_JOIN = 128;
+constexpr int NT_JOIN = 256;
+constexpr size_t JOIN_STATIC = NT_JOIN * 24;  // bytes of static shared memory
 
 template <int HD, typename T, bool LIST>
 __global__ void __launch_bounds__(NT_JOIN)
     paged_join_kernel(const __grid_constant__ DecodeParams p, int grid_decode, int by_head) {
   using S = DecodeShape<HD>;
-  constexpr int NG = NT_JOIN / 32, CB = 16;
+  constexpr int NG = NT_JOIN / 32, CB = 8;
   extern __shared__ int prefix[];  // [B + 1]
   __shared__ float4 wacc[NG][32];
   __shared__ float wm[NG][32], wz[NG][32];
+  static_assert(sizeof(wacc) + sizeof(wm) + sizeof(wz) == JOIN_STATIC, "join footprint");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = p.r;
+  griddep_launch_dependents();
   // Lengths are older than the decode kernel, which has waited for everything
   // before it: they are read ahead of the wait.
   count_units<LIST, S::UTOK>(p, prefix, nullptr, false);
