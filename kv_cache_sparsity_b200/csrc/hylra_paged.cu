@@ -20,6 +20,9 @@ namespace {
 
 constexpr size_t kSmemMax = 232448;  // 227 KB of dynamic shared memory per CTA
 constexpr size_t kSmemSM = 233472;   // 228 KB of shared memory per SM, 1 KB of it per CTA reserved
+// the largest table: 16384 pages of 16 tokens over eight CTAs, 8 heads, 1024 of them wanted
+static_assert(sizeof(SelectSmem) + 8 * 1024 * 8 + 2048 * 8 + 8 * 2048 * 8 <= kSmemMax,
+              "select kernel shared memory");
 constexpr int kCtasPerSM = 3;        // of the decode kernel, at most
 
 struct PagedLayout {
@@ -253,13 +256,20 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
 #undef HYLRA_DECODE
 }
 
+template <int HD, typename T, int R>
+int launch_select_r(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
+                    cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto kernel = paged_select_kernel<HD, T, R>;
+  if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
+  return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
+}
+
 template <int HD, typename T>
 int launch_select(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
                   cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  auto kernel = paged_select_kernel<HD, T>;
-  if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
-  return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
+  return p.r <= 4 ? launch_select_r<HD, T, 4>(p, cs, smem, nbh, dev, stream)
+                  : launch_select_r<HD, T, 8>(p, cs, smem, nbh, dev, stream);
 }
 
 template <int HD, typename T>
@@ -422,14 +432,12 @@ int hylra_paged_select(const hylra_paged_t* shape, const void* q, const void* ke
   p.max_pages = shape->max_pages;
   p.scale = shape->softmax_scale > 0.f ? (double)shape->softmax_scale
                                        : 1.0 / std::sqrt((double)shape->head_dim);
-  // CTAs per (sequence, KV head): until they fill the SMs a few times over, or
-  // their shares of the pages fit in shared memory
+  // CTAs per (sequence, KV head): as many as run at once, two to an SM, and more
+  // where a CTA would have over 1024 pages to sort (eight have 2048 at most)
   int cs = 1;
-  auto need = [&](int c) { return select_smem(p.r, (p.max_pages + c - 1) / c, p.max_pages); };
-  while (cs < MAX_CS && (nbh * cs * 2 <= 4LL * sms || need(cs) > kSmemMax)) cs *= 2;
-  if (need(cs) > kSmemMax) return HYLRA_ERR_UNSUPPORTED;
+  while (cs < MAX_CS && (nbh * cs * 2 <= 2LL * sms || (p.max_pages + cs - 1) / cs > 1024)) cs *= 2;
   p.ppc = (p.max_pages + cs - 1) / cs;
-  const size_t smem = need(cs);
+  const size_t smem = select_smem(p.r, p.ppc, cs, topk);
   cudaStream_t st = (cudaStream_t)stream;
   if (shape->head_dim == 128)
     return shape->dtype == HYLRA_BF16

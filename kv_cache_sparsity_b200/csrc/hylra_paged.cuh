@@ -747,159 +747,175 @@ struct SelectSmem {
   double wm[NW_SEL][GRP], wz[NW_SEL][GRP];
   double cm[MAX_CS][GRP], cz[MAX_CS][GRP];  // each CTA's maxima and sums, sent by the peers
   double m[GRP], f[GRP];
-  int hist[256];
-  int misc[4];
-  int wcnt[NW_SEL];
-  uint64_t sel[HYLRA_MAX_TOPK];
+  alignas(16) double q[GRP][4][34];  // a head's four quarters of the dims, 4 banks apart
 };
 
-// dynamic shared memory: SelectSmem, e[r][ppc] doubles, keys[max_pages] (rank 0's are used)
-inline __host__ __device__ size_t select_smem(int r, int ppc, int max_pages) {
-  return sizeof(SelectSmem) + (size_t)r * ppc * 8 + (size_t)max_pages * 4;
+inline __host__ __device__ int pow2_above(int x) {
+  int p = 1;
+  while (p < x) p <<= 1;
+  return p;
 }
 
-// 16-bit elements to double (exact)
+// Dynamic shared memory: SelectSmem, every CTA's best entries (sorted, a power of
+// two of them), this CTA's entries (a multiple of NT_SEL), the weights e[r][ppc].
+inline __host__ __device__ int select_best(int ppc, int k) { return pow2_above(k < ppc ? k : ppc); }
+inline __host__ __device__ int select_entries(int ppc) {
+  return ppc <= NT_SEL ? NT_SEL : pow2_above(ppc);
+}
+inline __host__ __device__ size_t select_smem(int r, int ppc, int cs, int k) {
+  return sizeof(SelectSmem) + (size_t)cs * select_best(ppc, k) * 8 +
+         (size_t)select_entries(ppc) * 8 + (size_t)r * ppc * 8;
+}
+
+// An fp32 value times 2^-896 as a double, by its bits: the fp32 exponent stands in
+// the double's field as it is, and the query is multiplied by 2^896 instead.
+// Two integer instructions, beside the products (the conversion instruction took
+// as long as they do).  Zeros stay zeros; infinity and NaN must be sorted out by
+// the caller.   x: a 16-bit value's fp32
+// pattern (its last three bits are 0).
+__device__ __forceinline__ double widen(uint32_t x) {
+  return __hiloint2double((int)((uint32_t)((int)x >> 3) & 0x8fffffffu), 0);
+}
+constexpr double WIDEN_UNIT = 0x1p896;
+
+// 16-bit elements as fp32 bit patterns
 template <typename T>
-__device__ __forceinline__ void widen2(uint32_t u, double& lo, double& hi) {
+__device__ __forceinline__ void unpack2(uint32_t u, uint32_t& lo, uint32_t& hi) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    lo = (double)__uint_as_float(u << 16);
-    hi = (double)__uint_as_float(u & 0xffff0000u);
+    lo = u << 16;
+    hi = u & 0xffff0000u;
   } else {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    lo = (double)f.x;
-    hi = (double)f.y;
+    lo = __float_as_uint(f.x);
+    hi = __float_as_uint(f.y);
   }
 }
 
-__device__ __forceinline__ void dmma_8x8x4(double (&d)[2], double a, double b) {
-  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
-               : "+d"(d[0]), "+d"(d[1])
-               : "d"(a), "d"(b));
+// The largest magnitude bits of two packed 16-bit values each (for infinity and NaN).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+}
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(uint32_t m) {
+  constexpr uint32_t INF = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  return (m & 0xffffu) >= INF || (m >> 16) >= INF;
 }
 
-// The kr largest (key, page) of keys[0..nc), key descending and index
-// ascending, sorted, into dst (as first + index).  kr <= nc.
-__device__ void select_top(const uint32_t* keys, SelectSmem& sm, int nc, int kr, int first,
-                           int32_t* dst) {
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  int P2 = 1;
-  while (P2 < kr) P2 <<= 1;
-  for (int i = tid; i < P2; i += NT_SEL) sm.sel[i] = 0ull;
-  if (tid == 0) sm.misc[2] = 0;
-  // radix select on the bit patterns (scores are >= 0: unsigned order is numeric)
-  uint32_t prefix = 0;
-  int remain = kr, shift = 32;
-  bool whole = kr == nc;  // every key at the threshold digit is taken
-  while (!whole && shift > 0) {
-    shift -= 8;
-    sm.hist[tid] = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < nc; i0 += NT_SEL) {
-      const int i = i0 + tid;
-      const uint32_t key = i < nc ? keys[i] : 0u;
-      const bool in = i < nc && (shift == 24 || ((key ^ prefix) >> (shift + 8)) == 0u);
-      const uint32_t digit = in ? ((key >> shift) & 255u) : 256u;
-      const uint32_t peers = __match_any_sync(0xffffffffu, digit);
-      if (in && (__ffs(peers) - 1) == lane) atomicAdd(&sm.hist[digit], __popc(peers));
-    }
-    __syncthreads();
-    if (wid == 0) {
-      int cnt[8], local = 0;
+// Compare-exchange over a warp's 32 * N values, value lane * N + i in register i:
+// neighbours at distance j < N are in one lane, the others a shuffle apart.
+template <int N>
+__device__ __forceinline__ void sort_pass(uint64_t (&v)[N], int lane, int j, int k) {
+  if (j < N) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cnt[i] = sm.hist[255 - 8 * lane - i];
-        local += cnt[i];
-      }
-      int incl = local;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
-      }
-      int acc = incl - local;
-      if (acc < remain && remain <= incl) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (acc < remain && remain <= acc + cnt[i]) {
-            sm.misc[0] = 255 - 8 * lane - i;
-            sm.misc[1] = remain - acc;
-            sm.misc[3] = cnt[i];
-          }
-          acc += cnt[i];
+      for (int jj = 1; jj < N; jj <<= 1)
+        if (jj == j && !(i & jj)) {
+          const uint64_t a = v[i], b = v[i | jj];
+          const bool swap = ((lane * N + i) & k) == 0 ? a < b : a > b;
+          v[i] = swap ? b : a;
+          v[i | jj] = swap ? a : b;
         }
-      }
-    }
-    __syncthreads();
-    prefix |= (uint32_t)sm.misc[0] << shift;
-    remain = sm.misc[1];
-    whole = sm.misc[3] == remain;
-    __syncthreads();
-  }
-  __syncthreads();
-  const bool all = kr == nc;
-  const uint32_t tau = all ? 0u : prefix >> shift;
-  int before = 0;  // equal keys at lower indices
-  for (int i0 = 0; i0 < nc; i0 += NT_SEL) {
-    const int i = i0 + tid;
-    const uint32_t key = i < nc ? keys[i] : 0u;
-    const uint32_t top = all ? 1u : key >> shift;
-    bool take = i < nc && top > tau;
-    const bool eq = i < nc && top == tau;
-    if (whole) {
-      take |= eq;
-    } else {
-      // equal keys beyond the wanted number: the lowest indices
-      const uint32_t mask = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) sm.wcnt[wid] = __popc(mask);
-      __syncthreads();
-      int mine = before + __popc(mask & ((1u << lane) - 1u)), sum = 0;
+  } else {
+    const int lj = j / N;
 #pragma unroll
-      for (int w = 0; w < NW_SEL; ++w) {
-        if (w < wid) mine += sm.wcnt[w];
-        sum += sm.wcnt[w];
-      }
-      take |= eq && mine < remain;
-      before += sum;
-      __syncthreads();
+    for (int i = 0; i < N; ++i) {
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, v[i], lj);
+      const bool larger = (((lane * N + i) & k) == 0) == ((lane & lj) == 0);
+      v[i] = larger == (v[i] > o) ? v[i] : o;
     }
-    if (take) {
-      const int at = atomicAdd(&sm.misc[2], 1);
-      if (at < kr) sm.sel[at] = ((uint64_t)key << 32) | (uint32_t)~(uint32_t)i;
+  }
+}
+
+// In how many of the nl sorted lists' entries (descending, len a power of two,
+// padded with zeros) does an entry exceed v: the lists in lock step, one select
+// per step, no branch.
+template <int NL>
+__device__ __forceinline__ int count_above(const uint64_t* lists, int pitch, int nl, int len,
+                                           uint64_t v) {
+  int pos[NL], sum = 0;
+#pragma unroll
+  for (int t = 0; t < NL; ++t) pos[t] = 0;
+  for (int step = len >> 1; step > 0; step >>= 1)
+#pragma unroll
+    for (int t = 0; t < NL; ++t)
+      if (t < nl) pos[t] += lists[t * pitch + pos[t] + step - 1] > v ? step : 0;
+#pragma unroll
+  for (int t = 0; t < NL; ++t)
+    if (t < nl) sum += pos[t] + (lists[t * pitch + pos[t]] > v ? 1 : 0);
+  return sum;
+}
+
+// Puts list[0..256 N) (distinct entries, zeros at the end) in descending order
+// into sorted, of which only the first `want` places matter.  Each warp sorts
+// 32 N of them in registers; an entry's place is how many entries of the warps'
+// lists exceed it.
+template <int N>
+__device__ void block_sort(uint64_t* list, uint64_t* sorted, int want) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint64_t v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = list[wid * 32 * N + lane * N + i];
+#pragma unroll 1
+  for (int k = 2; k <= 32 * N; k <<= 1)
+#pragma unroll 1
+    for (int j = k >> 1; j > 0; j >>= 1) sort_pass<N>(v, lane, j, k);
+#pragma unroll
+  for (int i = 0; i < N; ++i) list[wid * 32 * N + lane * N + i] = v[i];
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
+    uint64_t x = v[0];
+#pragma unroll
+    for (int t = 1; t < N; ++t) x = t == i ? v[t] : x;
+    if (x != 0ull && lane * N + i < want) {
+      const int at = count_above<NW_SEL>(list, 32 * N, NW_SEL, 32 * N, x);
+      if (at < want) sorted[at] = x;
     }
   }
   __syncthreads();
-  // bitonic sort, descending; empty places are 0, below every entry
-  for (int k = 2; k <= P2; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int t = tid; t < P2 / 2; t += NT_SEL) {
-        const int i = 2 * t - (t & (j - 1));
-        const uint64_t a = sm.sel[i], b = sm.sel[i + j];
-        const bool desc = (i & k) == 0;
-        if (desc ? a < b : a > b) {
-          sm.sel[i] = b;
-          sm.sel[i + j] = a;
-        }
-      }
-      __syncthreads();
-    }
-  for (int i = tid; i < kr; i += NT_SEL)
-    dst[i] = first + (int32_t)~(uint32_t)(sm.sel[i] & 0xffffffffull);
 }
 
-template <int HD, typename T>
-__global__ void __launch_bounds__(NT_SEL)
+// Grid (cs, B * Hkv), a cluster per (sequence, KV head).  The scores decide
+// between pages that are often nearly equal, and one order must come out whatever
+// the split: products of 16-bit values and their sums, the exponentials and the
+// sums over pages run in 64 bits, and a score is rounded once, to fp32.  So a
+// kernel with many pages is bound by the 64-bit units (r d products a page and
+// head at 64 a clock and SM, about the time that the means' 2 d bytes take from
+// memory at r = 4), one with few by the chain of steps.
+// Each CTA ranks its share of the pages by a sort of (score, page) pairs; an
+// entry's rank among all is the number of entries above it in every CTA's list.
+// R: r rounded up to 4 or 8.
+template <int HD, typename T, int R>
+__global__ void __launch_bounds__(NT_SEL, 2)
     paged_select_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_sel);
-  double* e = reinterpret_cast<double*>(smem_sel + sizeof(SelectSmem));  // [r][ppc]
-  uint32_t* keys = reinterpret_cast<uint32_t*>(e + (size_t)p.r * p.ppc);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int cs = (int)gridDim.x, rank = (int)blockIdx.x;  // one cluster per (b, h)
+  const int cs = (int)gridDim.x, rank = (int)blockIdx.x;
+  const int best = select_best(p.ppc, p.k);  // entries that a CTA may contribute, padded
+  uint64_t* lists = reinterpret_cast<uint64_t*>(smem_sel + sizeof(SelectSmem));  // [cs][best]
+  uint64_t* list = lists + cs * best;
+  double* e = reinterpret_cast<double*>(list + select_entries(p.ppc));  // [r][ppc]
   const int bh = (int)blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   cluster_arrive_relaxed();
   griddep_wait();
   const int psl = p.ps_log2;
-  const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status, h == 0 && rank == 0 && tid == 0);
+  // the query row by row, while the length is on its way
+  constexpr int DL = HD / 4, NV = DL / 8;
+  for (int i = tid; i < R * HD / 2; i += NT_SEL) {
+    const int g = i / (HD / 2), d = 2 * (i - g * (HD / 2));
+    uint32_t u = 0u, lo, hi;
+    if (g < p.r)
+      u = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) +
+                                                   ((size_t)b * p.Hq + (size_t)h * p.r + g) * HD + d));
+    unpack2<T>(u, lo, hi);
+    double* to = &sm.q[g][(d >> 3) & 3][(d >> 5) * 8 + (d & 7)];
+    to[0] = (double)__uint_as_float(lo) * WIDEN_UNIT;
+    to[1] = (double)__uint_as_float(hi) * WIDEN_UNIT;
+  }
+  const int n = checked_len(p.seqlens, b, p.max_pages << psl, p.status,
+                            h == 0 && rank == 0 && tid == 0);
   const int nb = (n + (1 << psl) - 1) >> psl;
   const int c0 = min(p.sink, nb);              // pages [c0, c1) are ranked
   const int c1 = max(c0, nb - p.recent);
@@ -920,73 +936,118 @@ __global__ void __launch_bounds__(NT_SEL)
   const int per = (nc + cs - 1) / cs;
   const int s0 = min(nc, rank * per), s1 = min(nc, s0 + per), np = s1 - s0;
 
-  // logits on the 64-bit matrix unit: 8 pages x 8 heads, lane l holds the dims
-  // (l % 4) * HD/4 .. of page l / 4 and of head l / 4
-  constexpr int DL = HD / 4;
+  // Logits: a warp takes 16 pages at a time, a lane a quarter of the dims (8 of every
+  // 32, so that four lanes read 64 bytes together) of pages row and row + 8.  Page
+  // ids run two steps ahead, the means one.
   const int row = lane >> 2, c = lane & 3;
-  double qd[DL];
-  {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(
-        static_cast<const T*>(p.q) + ((size_t)b * p.Hq + (size_t)h * p.r + min(row, p.r - 1)) * HD +
-        c * DL);
+  constexpr int STEP = NW_SEL * 16;
+  auto page_at = [&](int at) {
+    return at < np ? __ldcg(p.table + (size_t)b * p.max_pages + c0 + s0 + at) : -1;
+  };
+  auto load_mean = [&](int at, int pg, uint4 (&u)[NV]) {
+    const bool ok = pg >= 0 && pg < p.num_pages;
+    if (!ok && at < np) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const T*>(p.means) + ((size_t)(ok ? pg : 0) * p.Hkv + h) * HD + c * 8);
 #pragma unroll
-    for (int t = 0; t < DL / 8; ++t) {
-      const uint4 u = reinterpret_cast<const uint4*>(src)[t];
-      widen2<T>(u.x, qd[8 * t], qd[8 * t + 1]);
-      widen2<T>(u.y, qd[8 * t + 2], qd[8 * t + 3]);
-      widen2<T>(u.z, qd[8 * t + 4], qd[8 * t + 5]);
-      widen2<T>(u.w, qd[8 * t + 6], qd[8 * t + 7]);
-    }
-    if (row >= p.r)
+    for (int t = 0; t < NV; ++t) u[t] = at < np ? __ldcg(src + 4 * t) : make_uint4(0u, 0u, 0u, 0u);
+    return ok;
+  };
+  uint4 u[2][NV];
+  bool ok[2], okn[2] = {false, false};
+  int pgn[2];
 #pragma unroll
-      for (int t = 0; t < DL; ++t) qd[t] = 0.0;
+  for (int t = 0; t < 2; ++t) {
+    const int at = wid * 16 + row + 8 * t;
+    ok[t] = load_mean(at, page_at(at), u[t]);
+    pgn[t] = page_at(at + STEP);
   }
-  double mx[2] = {-INFINITY, -INFINITY};
-  for (int g0 = wid * 8; g0 < np; g0 += NW_SEL * 8) {
-    const int at = g0 + row;
-    int pg = -1;
-    if (at < np) {
-      pg = __ldcg(p.table + (size_t)b * p.max_pages + c0 + s0 + at);
-      if (pg < 0 || pg >= p.num_pages) {
-        pg = -1;
-        atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+  __syncthreads();  // the query
+  // after the sum over the quarters this lane holds page row + 8 * (c & 1) and
+  // heads hb .. hb + R/2 - 1
+  const int hb = (c >> 1) * (R / 2);
+  double mx[R / 2];
+#pragma unroll
+  for (int j = 0; j < R / 2; ++j) mx[j] = -INFINITY;
+  for (int g0 = wid * 16; g0 < np; g0 += STEP) {
+    uint4 un[2][NV];
+    if (g0 + STEP < np) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int at = g0 + STEP + row + 8 * t;
+        okn[t] = load_mean(at, pgn[t], un[t]);
+        pgn[t] = page_at(at + STEP);
       }
     }
-    double acc[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
-    uint4 u[DL / 8];
+    double acc[2][R];
 #pragma unroll
-    for (int t = 0; t < DL / 8; ++t) {
-      u[t] = make_uint4(0u, 0u, 0u, 0u);
-      if (pg >= 0)
-        u[t] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.means) +
-                                              ((size_t)pg * p.Hkv + h) * HD + c * DL)[t];
-    }
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int t = 0; t < DL / 8; ++t) {
-      const uint32_t v[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
+      for (int g = 0; g < R; ++g) acc[t][g] = 0.0;
+    uint32_t mag[2] = {0u, 0u};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        double x0, x1;
-        widen2<T>(v[s], x0, x1);
-        dmma_8x8x4(acc[0], x0, qd[8 * t + 2 * s]);
-        dmma_8x8x4(acc[1], x1, qd[8 * t + 2 * s + 1]);
+        double x[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t w = s == 0 ? u[t][v].x : s == 1 ? u[t][v].y : s == 2 ? u[t][v].z : u[t][v].w;
+          uint32_t lo, hi;
+          unpack2<T>(w, lo, hi);
+          x[t][0] = widen(lo);
+          x[t][1] = widen(hi);
+          mag[t] = max_abs2(mag[t], w);
+        }
+#pragma unroll
+        for (int g = 0; g < R; ++g) {
+          const double2 y = *reinterpret_cast<const double2*>(&sm.q[g][c][8 * v + 2 * s]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) acc[t][g] = fma(x[t][1], y.y, fma(x[t][0], y.x, acc[t][g]));
+        }
+      }
+    bool bad[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      bad[t] = any_nonfinite<T>(mag[t]);
+      bad[t] |= __shfl_xor_sync(0xffffffffu, (int)bad[t], 1) != 0;
+      bad[t] |= __shfl_xor_sync(0xffffffffu, (int)bad[t], 2) != 0;
+    }
+    // sum over the quarters, each exchange halving what a lane holds
+    double one[R], half[R / 2];
+#pragma unroll
+    for (int g = 0; g < R; ++g) {
+      const double keep = (c & 1) ? acc[1][g] : acc[0][g], give = (c & 1) ? acc[0][g] : acc[1][g];
+      one[g] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
+    }
+#pragma unroll
+    for (int j = 0; j < R / 2; ++j) {
+      const double keep = (c & 2) ? one[R / 2 + j] : one[j], give = (c & 2) ? one[j] : one[R / 2 + j];
+      half[j] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+    }
+    const int at = g0 + row + 8 * (c & 1);
+    const bool has = (c & 1) ? ok[1] : ok[0], nan = (c & 1) ? bad[1] : bad[0];
+#pragma unroll
+    for (int j = 0; j < R / 2; ++j) {
+      const double l = nan ? (double)NAN : has ? half[j] * p.scale : -INFINITY;
+      if (at < np && hb + j < p.r) {
+        e[(size_t)(hb + j) * p.ppc + at] = l;
+        mx[j] = fmax(mx[j], l);
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const double l = pg >= 0 ? (acc[0][j] + acc[1][j]) * p.scale : -INFINITY;
-      if (at < np && 2 * c + j < p.r) e[(size_t)(2 * c + j) * p.ppc + at] = l;
-      mx[j] = fmax(mx[j], at < np ? l : -INFINITY);
+    for (int t = 0; t < 2; ++t) {
+      ok[t] = okn[t];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) u[t][v] = un[t][v];
     }
   }
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    mx[0] = fmax(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
-    mx[1] = fmax(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
-  }
-  if (row == 0) {
-    sm.wm[wid][2 * c] = mx[0];
-    sm.wm[wid][2 * c + 1] = mx[1];
+  for (int j = 0; j < R / 2; ++j) {
+    mx[j] = fmax(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 1));
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) mx[j] = fmax(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], off));
+    if (row == 0 && (c & 1) == 0) sm.wm[wid][hb + j] = mx[j];
   }
   __syncthreads();
   if (tid < p.r) {
@@ -995,54 +1056,85 @@ __global__ void __launch_bounds__(NT_SEL)
     sm.m[tid] = m;
   }
   __syncthreads();
-  // e = exp(logit - this CTA's maximum), and its sum
-  for (int g = 0; g < p.r; ++g) {
+  // e = exp(logit - this CTA's maximum), and its sum: a head per warp, or
+  // several warps a head
+  const int wph = NW_SEL / p.r, g = wid % p.r, part = wid / p.r;
+  if (part < wph) {
     const double m = sm.m[g] == -INFINITY ? 0.0 : sm.m[g];
     double z = 0.0;
-    for (int i = tid; i < np; i += NT_SEL) {
+    for (int i = part * 32 + lane; i < np; i += wph * 32) {
       const double v = exp(e[(size_t)g * p.ppc + i] - m);
       e[(size_t)g * p.ppc + i] = v;
       z += v;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    if (lane == 0) sm.wz[wid][g] = z;
+    if (lane == 0) sm.wz[part][g] = z;
   }
   __syncthreads();
   cluster_wait_acquire();  // every CTA of the cluster runs: its shared memory may be written
   if (tid < cs * GRP) {
-    const int peer = tid / GRP, g = tid % GRP;
-    if (g < p.r) {
+    const int peer = tid / GRP, hg = tid % GRP;
+    if (hg < p.r) {
       double z = 0.0;
-      for (int w = 0; w < NW_SEL; ++w) z += sm.wz[w][g];
-      st_dsmem_f64(mapa_shared(smem_u32(&sm.cm[rank][g]), peer), sm.m[g]);
-      st_dsmem_f64(mapa_shared(smem_u32(&sm.cz[rank][g]), peer), z);
+      for (int w = 0; w < wph; ++w) z += sm.wz[w][hg];
+      st_dsmem_f64(mapa_shared(smem_u32(&sm.cm[rank][hg]), peer), sm.m[hg]);
+      st_dsmem_f64(mapa_shared(smem_u32(&sm.cz[rank][hg]), peer), z);
     }
   }
   cluster_sync_all();
-  if (tid < p.r) {
-    double M = -INFINITY, Z = 0.0;
-    for (int t = 0; t < cs; ++t) M = fmax(M, sm.cm[t][tid]);
-    for (int t = 0; t < cs; ++t)
-      if (sm.cm[t][tid] != -INFINITY) Z += sm.cz[t][tid] * exp(sm.cm[t][tid] - M);
-    sm.f[tid] = sm.m[tid] == -INFINITY ? 0.0 : exp(sm.m[tid] - M) / Z;
+  if (wid < p.r) {  // warp g: what this CTA's weights of head g are divided by
+    const double m = lane < cs ? sm.cm[lane][wid] : -INFINITY;
+    double M = m;
+#pragma unroll
+    for (int off = MAX_CS / 2; off > 0; off >>= 1)
+      M = fmax(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const double f = m == -INFINITY ? 0.0 : exp(m - M);
+    double Z = lane < cs ? f * sm.cz[lane][wid] : 0.0;
+#pragma unroll
+    for (int off = MAX_CS / 2; off > 0; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
+    if (lane == rank) sm.f[wid] = m == -INFINITY ? 0.0 : f / Z;
   }
   __syncthreads();
-  const uint32_t kbase = mapa_shared(smem_u32(keys), 0);
+  const int entries = select_entries(np);
   bool odd = false;
-  for (int i = tid; i < np; i += NT_SEL) {
-    double s = 0.0;
-    for (int g = 0; g < p.r; ++g) s += e[(size_t)g * p.ppc + i] * sm.f[g];
-    float key = (float)s;
-    if (!(key >= 0.f && key < INFINITY)) {
-      key = 0.f;
-      odd = true;
+  for (int i = tid; i < entries; i += NT_SEL) {
+    uint64_t v = 0ull;  // below every entry
+    if (i < np) {
+      double s = 0.0;
+      for (int t = 0; t < p.r; ++t) s += e[(size_t)t * p.ppc + i] * sm.f[t];
+      float key = (float)s;
+      if (!(key >= 0.f && key < INFINITY)) {
+        key = 0.f;
+        odd = true;
+      }
+      v = ((uint64_t)__float_as_uint(key) << 32) | (uint32_t)~(uint32_t)(s0 + i);
     }
-    st_dsmem_u32(kbase + (uint32_t)(s0 + i) * 4u, __float_as_uint(key));
+    list[i] = v;
   }
   if (odd) atomicOr(p.status, HYLRA_STATUS_NONFINITE);
-  cluster_sync_all();
-  if (rank == 0) select_top(keys, sm, nc, kr, c0, dst + forced);
+  uint64_t* own = lists + rank * best;
+  for (int i = tid; i < best; i += NT_SEL) own[i] = 0ull;
+  __syncthreads();
+  const int mine = min(kr, np);
+  switch (entries / NT_SEL) {
+    case 1: block_sort<1>(list, own, mine); break;
+    case 2: block_sort<2>(list, own, mine); break;
+    case 4: block_sort<4>(list, own, mine); break;
+    default: block_sort<8>(list, own, mine); break;  // a CTA has 2048 pages at most
+  }
+  if (cs > 1) {
+    for (int i = tid; i < best * cs; i += NT_SEL) {
+      const int peer = i / best, at = i - peer * best;
+      if (peer != rank) st_dsmem_u64(mapa_shared(smem_u32(own + at), peer), own[at]);
+    }
+    cluster_sync_all();
+  }
+  for (int i = tid; i < mine; i += NT_SEL) {
+    const uint64_t v = own[i];
+    const int at = cs > 1 ? count_above<MAX_CS>(lists, best, cs, best, v) : i;
+    if (at < kr) dst[forced + at] = c0 + (int32_t)~(uint32_t)(v & 0xffffffffull);
+  }
 }
 
 // ----------------------------------------------------------------- append
