@@ -273,11 +273,11 @@ int launch_select(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
 }
 
 template <int HD, typename T>
-int launch_append(const AppendParams& p, int tiles, int dev, cudaStream_t stream) {
+int launch_append(const AppendParams& p, unsigned ctas, int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_append_kernel<HD, T>;
   if (int rc = prepare(kernel, done, dev)) return rc;
-  return launch(kernel, dim3(tiles, p.Hkv), NT_APP, 0, stream, 1, p);
+  return launch(kernel, dim3(ctas), NT_APP, 0, stream, 1, p);
 }
 
 }  // namespace
@@ -345,8 +345,7 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
                        size_t workspace_bytes, hylra_stream_t stream) {
   int rc = check_paged(shape);
   if (rc || (rc = check_pool(shape))) return rc;
-  if (num_tokens < 0 || shape->num_kv_heads > 65535)
-    return num_tokens < 0 ? HYLRA_ERR_INVALID : HYLRA_ERR_UNSUPPORTED;
+  if (num_tokens < 0) return HYLRA_ERR_INVALID;
   const int64_t width = (int64_t)shape->num_kv_heads * shape->head_dim;
   if (num_tokens > 0 &&
       (bad_ptr(K_new, 16) || bad_ptr(V_new, 16) || bad_ptr(slot_map, 4) || new_stride < width ||
@@ -377,15 +376,16 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
   p.ps_log2 = log2_of(shape->page_size);
   p.num_slots = shape->num_pages * shape->page_size;
   // few tokens: a CTA each, so that they spread over the SMs
-  const long long rows = (long long)num_tokens * p.Hkv;
-  p.tile = (int)std::min<long long>(TILE_APP, std::max<long long>(1, rows / (4LL * sms)));
-  const int tiles = (num_tokens + p.tile - 1) / p.tile;
+  p.blocks = (int)((2 * width / 8 + COLS_APP - 1) / COLS_APP);
+  p.tile = std::min(std::min(TILE_APP, shape->page_size), std::max(1, num_tokens / (4 * sms)));
+  const long long ctas = (long long)p.blocks * (((long long)num_tokens + p.tile - 1) / p.tile);
+  if (ctas > INT_MAX) return HYLRA_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   if (shape->head_dim == 128)
-    return shape->dtype == HYLRA_BF16 ? launch_append<128, __nv_bfloat16>(p, tiles, dev, st)
-                                      : launch_append<128, __half>(p, tiles, dev, st);
-  return shape->dtype == HYLRA_BF16 ? launch_append<64, __nv_bfloat16>(p, tiles, dev, st)
-                                    : launch_append<64, __half>(p, tiles, dev, st);
+    return shape->dtype == HYLRA_BF16 ? launch_append<128, __nv_bfloat16>(p, (unsigned)ctas, dev, st)
+                                      : launch_append<128, __half>(p, (unsigned)ctas, dev, st);
+  return shape->dtype == HYLRA_BF16 ? launch_append<64, __nv_bfloat16>(p, (unsigned)ctas, dev, st)
+                                    : launch_append<64, __half>(p, (unsigned)ctas, dev, st);
 }
 
 int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,

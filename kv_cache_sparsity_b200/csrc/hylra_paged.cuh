@@ -1140,6 +1140,7 @@ __global__ void __launch_bounds__(NT_SEL, 2)
 // ----------------------------------------------------------------- append
 
 constexpr int NT_APP = 256;
+constexpr int COLS_APP = 128;  // 16-byte columns of a CTA
 constexpr int TILE_APP = 64;  // tokens per CTA, at most
 
 struct AppendParams {
@@ -1152,79 +1153,130 @@ struct AppendParams {
   uint32_t* status;
   long long new_stride, page_stride, head_stride, token_stride;
   int tokens, tile, Hkv, ps_log2, num_slots;
+  int blocks;  // column blocks of a token's K and V rows
 };
 
-// grid (token tiles, KV heads).  A CTA copies its tokens' rows of one head; a
-// token in the last row of its page makes the page full, and the CTA then
-// averages the page: rows of this call from the new keys (the tokens before
-// it, whose slots count down by one), earlier rows from the pool.
+// A run is a row of tokens in consecutive slots of one page.  A CTA owns the runs
+// that begin in its tile of tokens, for a block of 128 of the 16-byte columns of a
+// token's K and V: it copies their rows, each thread one column, and when a run fills
+// its page, the threads have summed the page's keys on the way.  Rows of the page
+// before the run come from the pool, or from the input where a token that was left out
+// parts two runs of this call.  Bound by memory: two rows read and two written a
+// token.  68 000 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
+// copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
+// took 127-135 us, two rows in flight per thread do as well as four (eight: 118), and
+// 64 columns a CTA lose a fifth with 16-token pages.
 template <int HD, typename T>
 __global__ void __launch_bounds__(NT_APP)
     paged_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int VPR = HD / 8;          // 16-byte vectors per row
-  constexpr int RP = NT_APP / VPR;     // rows at a time
-  __shared__ int slot_s[TILE_APP];
-  __shared__ float part[NT_APP][9];    // 9: threads of a column land in different banks
-  __shared__ bool fresh[MAX_PAGE];         // rows of a full page that this call brings
-  const int tid = threadIdx.x, v = tid % VPR, rl = tid / VPR;
-  const int h = (int)blockIdx.y, t0 = (int)blockIdx.x * p.tile;
-  const int cnt = min(p.tile, p.tokens - t0);
-  const int ps = 1 << p.ps_log2;
+  __shared__ float part[NT_APP][9];  // 9: a warp's columns fall into different banks
+  __shared__ int slots[TILE_APP + 2 * MAX_PAGE];  // of the tokens a page before the tile and on
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int blk = (int)(blockIdx.x % (unsigned)p.blocks);
+  const long long first = (long long)(blockIdx.x / (unsigned)p.blocks) * p.tile;
+  const int width = p.Hkv * (HD / 8);  // columns of K, and of V
+  const int cols = min(COLS_APP, 2 * width - blk * COLS_APP);
+  const int nrow = NT_APP / cols, rl = tid / cols;  // rows at a time
+  const int ckv = blk * COLS_APP + tid - rl * cols;   // column of the token's K, then V
+  const bool keys = ckv < width, active = rl < nrow;
+  const int cv = keys ? ckv : ckv - width, h = cv / (HD / 8), v = cv % (HD / 8);
+  const int psl = p.ps_log2, ps = 1 << psl;
+  const uint16_t* src = (keys ? p.K_new : p.V_new) + (size_t)cv * 8;
+  uint16_t* pool = (keys ? p.K : p.V) + (size_t)h * p.head_stride + v * 8;
   griddep_wait();
-  for (int i = tid; i < cnt; i += NT_APP) {
-    int s = __ldcg(p.slots + t0 + i);
+  const int tb = (int)first;
+  for (int i = tid; i < p.tile + 2 * ps; i += NT_APP) {
+    const long long t = (long long)tb - ps + i;
+    int s = t >= 0 && t < p.tokens ? __ldcg(p.slots + t) : -1;
     if (s < 0 || s >= p.num_slots) {
-      if (s != -1 && h == 0) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
+      if (s != -1 && blk == 0 && i >= ps && i < ps + p.tile)
+        atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
       s = -1;
     }
-    slot_s[i] = s;
+    slots[i] = s;
   }
   __syncthreads();
-  for (int i = rl; i < cnt; i += RP) {
-    const int s = slot_s[i];
-    if (s < 0) continue;
-    const size_t src = (size_t)(t0 + i) * p.new_stride + (size_t)h * HD + v * 8;
-    const size_t dst = (size_t)(s >> p.ps_log2) * p.page_stride + (size_t)h * p.head_stride +
-                       (size_t)(s & (ps - 1)) * p.token_stride + v * 8;
-    const uint4 kv = *reinterpret_cast<const uint4*>(p.K_new + src);
-    const uint4 vv = *reinterpret_cast<const uint4*>(p.V_new + src);
-    *reinterpret_cast<uint4*>(p.K + dst) = kv;
-    *reinterpret_cast<uint4*>(p.V + dst) = vv;
-  }
-  if (!p.means) return;
-  for (int i = 0; i < cnt; ++i) {
-    const int s = slot_s[i];  // the same in every thread
-    if (s < 0 || (s & (ps - 1)) != ps - 1) continue;
-    const int t = t0 + i, page = s >> p.ps_log2;
-    // row ps-1-back is new if the token `back` places before t has its slot
-    if (tid < ps) {
-      const int back = ps - 1 - tid;
-      fresh[tid] = t >= back && __ldcg(p.slots + t - back) == s - back;
+  const int* tile = slots + ps;  // tile[i]: token tb + i, i from -ps to tile + ps - 1
+  auto row_at = [&](int s) {
+    return reinterpret_cast<uint4*>(pool + (size_t)(s >> psl) * p.page_stride +
+                                    (size_t)(s & (ps - 1)) * p.token_stride);
+  };
+  auto begins = [&](int l) {  // a run begins at token l of the tile
+    return l < p.tile && tile[l] >= 0 &&
+           ((tile[l] & (ps - 1)) == 0 || tile[l - 1] < 0 || tile[l - 1] != tile[l] - 1);
+  };
+  uint64_t starts = (uint64_t)__ballot_sync(0xffffffffu, begins(lane)) |
+                    (uint64_t)__ballot_sync(0xffffffffu, begins(lane + 32)) << 32;
+  while (starts) {
+    const int l = __ffsll((long long)starts) - 1;
+    starts &= starts - 1;
+    const int s0 = tile[l], off = s0 & (ps - 1), t = tb + l;
+    // length of the run: up to the page's end or the first slot out of line
+    int len = 0;
+    for (bool whole = true; whole && len < ps - off;) {
+      const int i = len + lane;
+      const uint32_t out =
+          ~__ballot_sync(0xffffffffu, off + i < ps && tile[l + min(i, ps - 1)] == s0 + i);
+      whole = out == 0u;
+      len += whole ? 32 : __ffs(out) - 1;
     }
-    __syncthreads();
+    const bool fills = p.means != nullptr && off + len == ps;
     float sum[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-    for (int row = rl; row < ps; row += RP) {
-      const uint16_t* src =
-          fresh[row] ? p.K_new + (size_t)(t - (ps - 1 - row)) * p.new_stride + (size_t)h * HD
-                     : p.K + (size_t)page * p.page_stride + (size_t)h * p.head_stride +
-                           (size_t)row * p.token_stride;
-      const uint4 u = *reinterpret_cast<const uint4*>(src + v * 8);
+    auto add = [&](const uint4& u) {
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         sum[2 * k] += Elem<T>::value((uint16_t)(w[k] & 0xffffu));
         sum[2 * k + 1] += Elem<T>::value((uint16_t)(w[k] >> 16));
       }
+    };
+    constexpr int U = 2;  // rows in flight per thread
+    for (int i0 = active ? rl : len; i0 < len; i0 += nrow * U) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * nrow < len)
+          x[u] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)(t + i0 + u * nrow) * p.new_stride));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * nrow < len) {
+          *row_at(s0 + i0 + u * nrow) = x[u];
+          if (fills) add(x[u]);
+        }
+    }
+    if (!fills) continue;
+    // rows before the run: from the pool, or from this call
+    for (int i0 = active && keys ? rl : off; i0 < off; i0 += nrow * U) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * nrow;
+        if (i >= off) continue;
+        const uint4* from = row_at(s0 - off + i);
+        if (tile[l - off + i] == s0 - off + i)
+          from = reinterpret_cast<const uint4*>(src + (size_t)(t - off + i) * p.new_stride);
+        x[u] = __ldcg(from);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * nrow < off) add(x[u]);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) part[tid][k] = sum[k];
     __syncthreads();
-    if (tid < HD) {
-      float total = 0.f;
-      for (int q = 0; q < RP; ++q) total += part[q * VPR + tid / 8][tid % 8];
-      p.means[((size_t)page * p.Hkv + h) * HD + tid] = Elem<T>::bits(total / (float)ps);
+    if (rl == 0 && keys) {
+      for (int q = 1; q < nrow; ++q)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += part[tid + q * cols][k];
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = (uint32_t)Elem<T>::bits(sum[2 * k] / (float)ps) |
+               (uint32_t)Elem<T>::bits(sum[2 * k + 1] / (float)ps) << 16;
+      *reinterpret_cast<uint4*>(p.means + (size_t)(s0 >> psl) * p.Hkv * HD + (size_t)cv * 8) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncthreads();
   }
@@ -1361,46 +1413,64 @@ __global__ void __launch_bounds__(NT_TAB)
   __syncthreads();
   const int left = sm.left, used = avail - left, cu_end = sm.cu[p.B];
 
-  auto owner = [&](const int* start, int i) {  // last request whose start is <= i
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (start[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+  // The last request whose start is <= i[v], for four places at once: the same
+  // number of steps for all, so that the searches overlap.
+  int top = 1;
+  while (2 * top < p.B) top *= 2;
+  auto owners = [&](const int* start, const int (&i)[4], int (&b)[4]) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) b[v] = 0;
+    for (int step = top; step > 0; step >>= 1)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int at = b[v] + step;
+        if (at < p.B && start[at] <= i[v]) b[v] = at;
+      }
   };
-  auto popped = [&](int nth) {
-    const int pg = __ldcg(p.free_pages + (avail - 1 - nth));
-    return pg >= 0 && pg < p.num_pages ? pg : -1;
-  };
-  const int step = (int)gridDim.x * NT_TAB;
   bool odd = false;
-  for (int a = (int)blockIdx.x * NT_TAB + tid; a < used; a += step) {
-    const int b = owner(sm.first, a);
-    const int pg = popped(a);
-    odd |= pg < 0;
-    p.table[(size_t)b * p.max_pages + ((sm.held[b] + ps - 1) >> psl) + (a - sm.first[b])] = pg;
+  const int stride = 4 * (int)gridDim.x * NT_TAB;
+  // a thread's four places are NT_TAB apart: a warp's stores stay together
+  for (int base = (int)blockIdx.x * 4 * NT_TAB + tid; base < used; base += stride) {
+    int a[4], b[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) a[v] = min(base + v * NT_TAB, used - 1);
+    owners(sm.first, a, b);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (base + v * NT_TAB >= used) break;
+      int pg = __ldcg(p.free_pages + (avail - 1 - a[v]));
+      if (pg < 0 || pg >= p.num_pages) {
+        pg = -1;
+        odd = true;
+      }
+      p.table[(size_t)b[v] * p.max_pages + ((sm.held[b[v]] + ps - 1) >> psl) +
+              (a[v] - sm.first[b[v]])] = pg;
+    }
   }
-  for (long long tl = (long long)blockIdx.x * NT_TAB + tid; tl < p.slot_cap; tl += step) {
-    const int t = (int)tl;
-    int slot = -1;
-    if (t < cu_end) {
-      const int b = owner(sm.cu, t);
-      if (sm.held[b] >= 0) {
-        const int pos = sm.held[b] + (t - sm.cu[b]), j = pos >> psl;
-        const int have = (sm.held[b] + ps - 1) >> psl;
-        int pg;
-        if (j < have) {
-          pg = __ldcg(p.table + (size_t)b * p.max_pages + j);
-          if (pg < 0 || pg >= p.num_pages) pg = -1;
-        } else {
-          pg = popped(sm.first[b] + j - have);
-        }
-        odd |= pg < 0;
-        if (pg >= 0) slot = (pg << psl) + (pos & (ps - 1));
+  for (long long base = (long long)blockIdx.x * 4 * NT_TAB + tid; base < p.slot_cap;
+       base += stride) {
+    int t[4], b[4], pg[4], pos[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) t[v] = (int)min(base + v * NT_TAB, (long long)p.slot_cap - 1);
+    owners(sm.cu, t, b);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int held = sm.held[b[v]];
+      pg[v] = pos[v] = -1;
+      if (t[v] < cu_end && held >= 0) {
+        pos[v] = held + (t[v] - sm.cu[b[v]]);
+        const int j = pos[v] >> psl, have = (held + ps - 1) >> psl;
+        pg[v] = __ldcg(j < have ? p.table + (size_t)b[v] * p.max_pages + j
+                                : p.free_pages + (avail - 1 - (sm.first[b[v]] + j - have)));
       }
     }
-    p.slots[t] = slot;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const bool ok = pg[v] >= 0 && pg[v] < p.num_pages;
+      odd |= pos[v] >= 0 && !ok;
+      if (base + v * NT_TAB < p.slot_cap)
+        p.slots[t[v]] = ok ? (pg[v] << psl) + (pos[v] & (ps - 1)) : -1;
+    }
   }
   if (odd) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
   if (gridDim.x > 1) {

@@ -397,45 +397,69 @@ def _want(what, t, dtype, shape, dev, dense=True):
 
 # A decode step makes a handful of these calls per layer, and a small one costs
 # the GPU less than its checks cost the host: each call tests all its tensors in
-# one expression and looks for the one to name only when that fails.
+# one expression, against tuples made once per shape, and looks for the one to
+# name only when that fails.
 
 
-def _want_pools(s: PagedShape, dtype, K, V, dev):
-    shape = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)
-    strides = (s.page_stride, s.head_stride, s.token_stride, 1)
-    if (K.dtype is dtype and V.dtype is dtype and K.shape == shape and V.shape == shape
-            and K.stride() == strides and V.stride() == strides and K.get_device() == dev
+class _Forms:
+    """What the tensors of a PagedShape's calls must look like."""
+
+    def __init__(self, s: PagedShape):
+        import torch
+        self.key = bytes(s)
+        self.torch = torch
+        self.dtype = torch.bfloat16 if s.dtype == BF16 else torch.float16
+        self.pool = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)
+        self.strides = (s.page_stride, s.head_stride, s.token_stride, 1)
+        self.q = (s.batch, s.num_q_heads, s.head_dim)
+        self.table = (s.batch, s.max_pages)
+        self.lens = (s.batch,)
+        self.lse = (s.batch, s.num_q_heads)
+        self.heads = (s.batch, s.num_kv_heads)
+        self.means = (s.num_pages, s.num_kv_heads, s.head_dim)
+        self.ref = ctypes.byref(s)
+
+
+def _forms(s: PagedShape) -> _Forms:
+    f = s.__dict__.get("_forms")
+    if f is None or f.key != bytes(s):  # made again when a field has changed
+        f = s.__dict__["_forms"] = _Forms(s)
+    return f
+
+
+def _want_pools(f: _Forms, K, V, dev):
+    if (K.dtype is f.dtype and V.dtype is f.dtype and K.shape == f.pool and V.shape == f.pool
+            and K.stride() == f.strides and V.stride() == f.strides and K.get_device() == dev
             and V.get_device() == dev):
         return
     for what, t in (("K_pages", K), ("V_pages", V)):
-        _want(what, t, dtype, shape, dev, dense=False)
+        _want(what, t, f.dtype, f.pool, dev, dense=False)
         # the stride of a dimension of one element has no meaning
-        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
-            raise ValueError(f"{what}: strides {t.stride()} differ from the shape's {strides}")
+        if any(n > 1 and a != b for n, a, b in zip(f.pool, t.stride(), f.strides)):
+            raise ValueError(f"{what}: strides {t.stride()} differ from the shape's {f.strides}")
 
 
-def _want_query(s: PagedShape, torch, dtype, q, block_table, seqlens, dev):
-    B, i32 = s.batch, torch.int32
-    qshape, tshape = (B, s.num_q_heads, s.head_dim), (B, s.max_pages)
-    if (q.dtype is dtype and block_table.dtype is i32 and seqlens.dtype is i32
-            and q.shape == qshape and block_table.shape == tshape and seqlens.shape == (B,)
+def _want_query(f: _Forms, q, block_table, seqlens, dev):
+    i32 = f.torch.int32
+    if (q.dtype is f.dtype and block_table.dtype is i32 and seqlens.dtype is i32
+            and q.shape == f.q and block_table.shape == f.table and seqlens.shape == f.lens
             and q.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()
             and q.get_device() == dev and block_table.get_device() == dev
             and seqlens.get_device() == dev):
         return
-    _want("q", q, dtype, qshape, dev)
-    _want("block_table", block_table, i32, tshape, dev)
-    _want("seqlens", seqlens, i32, (B,), dev)
+    _want("q", q, f.dtype, f.q, dev)
+    _want("block_table", block_table, i32, f.table, dev)
+    _want("seqlens", seqlens, i32, f.lens, dev)
 
 
-def _want_result(s: PagedShape, torch, out, lse, dev):
-    _want("out", out, torch.float32, (s.batch, s.num_q_heads, s.head_dim), dev)
-    if lse is not None:
-        _want("lse", lse, torch.float32, (s.batch, s.num_q_heads), dev)
-
-
-def _paged_dtype(torch, s: PagedShape):
-    return torch.bfloat16 if s.dtype == BF16 else torch.float16
+def _want_result(f: _Forms, out, lse, dev):
+    f32 = f.torch.float32
+    if not (out.dtype is f32 and out.shape == f.q and out.is_contiguous()
+            and out.get_device() == dev):
+        _want("out", out, f32, f.q, dev)
+    if lse is not None and not (lse.dtype is f32 and lse.shape == f.lse and lse.is_contiguous()
+                                and lse.get_device() == dev):
+        _want("lse", lse, f32, f.lse, dev)
 
 
 def _paged_call(torch, entry, ws, dev, stream, *args):
@@ -454,19 +478,32 @@ def _paged_call(torch, entry, ws, dev, stream, *args):
 def paged_tables(shape: PagedShape, cached_lens, new_lens, free_pages, free_count, block_table,
                  seqlens_out, cu_new, slot_map, free_count_out, ws, stream=None):
     """Pages, slots and lengths of a step's new tokens (all int32)."""
-    import torch
-    dev, B, i32 = ws.get_device(), shape.batch, torch.int32
+    f = _forms(shape)
+    dev, i32, B = ws.get_device(), f.torch.int32, f.lens[0]
     nfree, nslots = free_pages.numel(), slot_map.numel()
-    one = (("cached_lens", cached_lens, B), ("new_lens", new_lens, B),
-           ("free_pages", free_pages, nfree), ("free_count", free_count, 1),
-           ("seqlens_out", seqlens_out, B), ("cu_new", cu_new, B + 1),
-           ("slot_map", slot_map, nslots), ("free_count_out", free_count_out, 1),
-           ("block_table", block_table, B * shape.max_pages))
-    for what, t, n in one:
-        if not (t.dtype is i32 and t.numel() == n and t.is_contiguous()
-                and t.get_device() == dev):
-            _want(what, t, i32, (B, shape.max_pages) if t is block_table else (n,), dev)
-    _paged_call(torch, (_lib or load()).hylra_paged_tables, ws, dev, stream, ctypes.byref(shape),
+    if not (cached_lens.dtype is i32 and new_lens.dtype is i32 and free_pages.dtype is i32
+            and free_count.dtype is i32 and block_table.dtype is i32 and seqlens_out.dtype is i32
+            and cu_new.dtype is i32 and slot_map.dtype is i32 and free_count_out.dtype is i32
+            and cached_lens.shape == f.lens and new_lens.shape == f.lens
+            and free_pages.dim() == 1 and free_count.numel() == 1 and block_table.shape == f.table
+            and seqlens_out.shape == f.lens and cu_new.numel() == B + 1 and slot_map.dim() == 1
+            and free_count_out.numel() == 1 and cached_lens.is_contiguous()
+            and new_lens.is_contiguous() and free_pages.is_contiguous()
+            and block_table.is_contiguous() and seqlens_out.is_contiguous()
+            and cu_new.is_contiguous() and slot_map.is_contiguous()
+            and cached_lens.get_device() == dev and new_lens.get_device() == dev
+            and free_pages.get_device() == dev and free_count.get_device() == dev
+            and block_table.get_device() == dev and seqlens_out.get_device() == dev
+            and cu_new.get_device() == dev and slot_map.get_device() == dev
+            and free_count_out.get_device() == dev):
+        for what, t, n in (("cached_lens", cached_lens, f.lens), ("new_lens", new_lens, f.lens),
+                           ("free_pages", free_pages, (nfree,)), ("free_count", free_count, (1,)),
+                           ("block_table", block_table, f.table),
+                           ("seqlens_out", seqlens_out, f.lens), ("cu_new", cu_new, (B + 1,)),
+                           ("slot_map", slot_map, (nslots,)),
+                           ("free_count_out", free_count_out, (1,))):
+            _want(what, t, i32, n, dev)
+    _paged_call(f.torch, (_lib or load()).hylra_paged_tables, ws, dev, stream, f.ref,
                 cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), nfree,
                 free_count.data_ptr(), block_table.data_ptr(), seqlens_out.data_ptr(),
                 cu_new.data_ptr(), slot_map.data_ptr(), nslots, free_count_out.data_ptr())
@@ -476,61 +513,75 @@ def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, ke
                  stream=None):
     """K_new / V_new [T, Hkv, d] (each token's heads adjacent, tokens at any stride) into the
     pools; key_means [num_pages, Hkv, d] or None."""
-    import torch
-    dev, t = ws.get_device(), _paged_dtype(torch, shape)
-    n, H, d = slot_map.numel(), shape.num_kv_heads, shape.head_dim
-    _want("slot_map", slot_map, torch.int32, (n,), dev)
-    for what, x in (("K_new", K_new), ("V_new", V_new)):
-        _want(what, x, t, (n, H, d), dev, dense=False)
-        if n and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
-            raise ValueError(f"{what}: a token's heads must be adjacent")
-    stride = K_new.stride(0) if n > 1 else H * d
-    if n > 1 and V_new.stride(0) != stride:
+    f = _forms(shape)
+    dev, t, n = ws.get_device(), f.dtype, slot_map.numel()
+    H, d = f.means[1], f.means[2]
+    rows, ks, vs = (n, H, d), K_new.stride(), V_new.stride()
+    if not (slot_map.dtype is f.torch.int32 and slot_map.dim() == 1 and slot_map.is_contiguous()
+            and slot_map.get_device() == dev and K_new.dtype is t and V_new.dtype is t
+            and K_new.shape == rows and V_new.shape == rows and K_new.get_device() == dev
+            and V_new.get_device() == dev):
+        _want("slot_map", slot_map, f.torch.int32, (n,), dev)
+        _want("K_new", K_new, t, rows, dev, dense=False)
+        _want("V_new", V_new, t, rows, dev, dense=False)
+    if n and (ks[2] != 1 or vs[2] != 1 or (H > 1 and (ks[1] != d or vs[1] != d))):
+        raise ValueError("K_new and V_new: a token's heads must be adjacent")
+    if n > 1 and ks[0] != vs[0]:
         raise ValueError("K_new and V_new must have the same token stride")
-    _want_pools(shape, t, K_pages, V_pages, dev)
-    if key_means is not None:
-        _want("key_means", key_means, t, (shape.num_pages, H, d), dev)
-    _paged_call(torch, (_lib or load()).hylra_paged_append, ws, dev, stream, ctypes.byref(shape),
-                K_new.data_ptr(), V_new.data_ptr(), stride, slot_map.data_ptr(), n,
-                K_pages.data_ptr(), V_pages.data_ptr(), _ptr(key_means))
+    _want_pools(f, K_pages, V_pages, dev)
+    if key_means is not None and not (key_means.dtype is t and key_means.shape == f.means
+                                      and key_means.is_contiguous()
+                                      and key_means.get_device() == dev):
+        _want("key_means", key_means, t, f.means, dev)
+    _paged_call(f.torch, (_lib or load()).hylra_paged_append, ws, dev, stream, f.ref,
+                K_new.data_ptr(), V_new.data_ptr(), ks[0] if n > 1 else H * d,
+                slot_map.data_ptr(), n, K_pages.data_ptr(), V_pages.data_ptr(),
+                None if key_means is None else key_means.data_ptr())
 
 
 def paged_decode(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, out, ws, lse=None,
                  stream=None):
     """Attention of one query token per sequence over its pages; lse: fp32 [B, Hq] or None."""
-    import torch
-    dev, t = ws.get_device(), _paged_dtype(torch, shape)
-    _want_query(shape, torch, t, q, block_table, seqlens, dev)
-    _want_pools(shape, t, K_pages, V_pages, dev)
-    _want_result(shape, torch, out, lse, dev)
-    _paged_call(torch, (_lib or load()).hylra_paged_decode, ws, dev, stream, ctypes.byref(shape),
+    f, dev = _forms(shape), ws.get_device()
+    _want_query(f, q, block_table, seqlens, dev)
+    _want_pools(f, K_pages, V_pages, dev)
+    _want_result(f, out, lse, dev)
+    _paged_call(f.torch, (_lib or load()).hylra_paged_decode, ws, dev, stream, f.ref,
                 q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
-                seqlens.data_ptr(), out.data_ptr(), _ptr(lse))
+                seqlens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr())
+
+
+def _want_list(f: _Forms, page_idx, dev):
+    k = page_idx.shape[-1]
+    if not (page_idx.dtype is f.torch.int32 and page_idx.shape == (*f.heads, k)
+            and page_idx.is_contiguous() and page_idx.get_device() == dev):
+        _want("page_idx", page_idx, f.torch.int32, (*f.heads, k), dev)
+    return k
 
 
 def paged_select(shape: PagedShape, q, key_means, block_table, seqlens, page_idx, ws, sink=1,
                  recent=1, stream=None):
     """The most promising pages of each (sequence, KV head) into page_idx int32 [B, Hkv, k]."""
-    import torch
-    dev, t, k = ws.get_device(), _paged_dtype(torch, shape), page_idx.shape[-1]
-    _want_query(shape, torch, t, q, block_table, seqlens, dev)
-    _want("key_means", key_means, t, (shape.num_pages, shape.num_kv_heads, shape.head_dim), dev)
-    _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
-    _paged_call(torch, (_lib or load()).hylra_paged_select, ws, dev, stream, ctypes.byref(shape),
-                q.data_ptr(), key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), k,
-                sink, recent, page_idx.data_ptr())
+    f, dev = _forms(shape), ws.get_device()
+    _want_query(f, q, block_table, seqlens, dev)
+    if not (key_means.dtype is f.dtype and key_means.shape == f.means
+            and key_means.is_contiguous() and key_means.get_device() == dev):
+        _want("key_means", key_means, f.dtype, f.means, dev)
+    k = _want_list(f, page_idx, dev)
+    _paged_call(f.torch, (_lib or load()).hylra_paged_select, ws, dev, stream, f.ref,
+                q.data_ptr(), key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
+                k, sink, recent, page_idx.data_ptr())
 
 
 def paged_decode_topk(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, page_idx, out,
                       ws, lse=None, stream=None):
     """paged_decode over the pages listed in page_idx int32 [B, Hkv, k]."""
-    import torch
-    dev, t, k = ws.get_device(), _paged_dtype(torch, shape), page_idx.shape[-1]
-    _want_query(shape, torch, t, q, block_table, seqlens, dev)
-    _want_pools(shape, t, K_pages, V_pages, dev)
-    _want("page_idx", page_idx, torch.int32, (shape.batch, shape.num_kv_heads, k), dev)
-    _want_result(shape, torch, out, lse, dev)
-    _paged_call(torch, (_lib or load()).hylra_paged_decode_topk, ws, dev, stream,
-                ctypes.byref(shape), q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
-                block_table.data_ptr(), seqlens.data_ptr(), page_idx.data_ptr(), k,
-                out.data_ptr(), _ptr(lse))
+    f, dev = _forms(shape), ws.get_device()
+    _want_query(f, q, block_table, seqlens, dev)
+    _want_pools(f, K_pages, V_pages, dev)
+    k = _want_list(f, page_idx, dev)
+    _want_result(f, out, lse, dev)
+    _paged_call(f.torch, (_lib or load()).hylra_paged_decode_topk, ws, dev, stream, f.ref,
+                q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+                seqlens.data_ptr(), page_idx.data_ptr(), k, out.data_ptr(),
+                None if lse is None else lse.data_ptr())
