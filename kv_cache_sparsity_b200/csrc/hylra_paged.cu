@@ -174,26 +174,34 @@ int launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? HYLRA_OK : HYLRA_ERR_CUDA;
 }
 
+// The decode kernel's ring stages, CTAs per SM and shared memory for a batch:
+// three CTAs with two stages each; where a large batch's lengths do not fit beside
+// them, two with three.
+struct DecodePlan {
+  int nst, ctas;
+  size_t smem;
+};
+template <int HD, typename T>
+DecodePlan decode_plan(int B) {
+  constexpr int SPLIT = Elem<T>::SPLIT;
+  DecodePlan pl{2, kCtasPerSM, 0};
+  auto fits = [&] { return (size_t)pl.ctas * (decode_smem<HD, SPLIT>(pl.nst, B) + 1024) <= kSmemSM; };
+  if (!fits()) pl = DecodePlan{3, 2, 0};
+  if (!fits()) pl.nst = 2;
+  pl.smem = decode_smem<HD, SPLIT>(pl.nst, B);
+  return pl;
+}
+
 template <int HD, typename T, bool LIST>
 int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& p, int sms,
                   int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_decode_kernel<HD, T, LIST>;
   if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
-  // three CTAs to an SM with two stages each; where a large batch's lengths do
-  // not fit beside them, two with three
-  int ctas = kCtasPerSM;
-  p.nst = 2;
-  auto fits = [&] {
-    return (size_t)ctas * (decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B) + 1024) <= kSmemSM;
-  };
-  if (!fits()) {
-    ctas = 2;
-    p.nst = 3;
-    if (!fits()) p.nst = 2;
-  }
-  const int G = std::min(ctas * sms, MAX_GRID);
-  const size_t smem = decode_smem<HD, Elem<T>::SPLIT>(p.nst, p.B);
+  const DecodePlan pl = decode_plan<HD, T>(p.B);
+  p.nst = pl.nst;
+  const int G = std::min(pl.ctas * sms, MAX_GRID);
+  const size_t smem = pl.smem;
   if (int rc = launch(kernel, dim3(G), NTHR, smem, stream, 1, tmK, tmV, p)) return rc;
   // fewer heads than CTAs: a CTA per head and 32 float4 columns; else a CTA per
   // decode CTA (at most one head that it holds in part ends after it)
@@ -257,11 +265,12 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
 }
 
 template <int HD, typename T, int R>
-int launch_select_r(const SelectParams& p, int cs, size_t smem, int nbh, int dev,
-                    cudaStream_t stream) {
+int launch_select_r(const SelectParams& p, int cs, size_t smem, int nbh, int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_select_kernel<HD, T, R>;
   if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
+  // its CTAs start beside the join of a call before: the decode kernel's footprint
+  smem = std::max(smem, decode_plan<HD, T>(p.B).smem);
   return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
 }
 

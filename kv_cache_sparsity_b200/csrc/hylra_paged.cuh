@@ -11,11 +11,13 @@
 //
 // Every kernel is launched as a programmatic dependent and waits for the
 // preceding kernel before its first access to global memory (but for the join's,
-// see there).  Only the decode kernel lets its dependent start early, which is
-// the join that is launched with it.  A decode kernel that started beside small
-// CTAs of another found its SMs' shared memory in pieces: where two of its CTAs
-// lay around a small one, the third had no room until one of them ended, and the
-// kernel took half as long again (16 sequences of up to 128K: 960 us, not 620).
+// see there).  Only the decode kernel and the join let their dependents start early.
+// What may then share an SM with decode CTAs that start has the decode kernel's
+// shared memory footprint (the join; the selection, where it needs no more): a decode
+// kernel that started beside smaller CTAs found its SMs' shared memory in pieces, and
+// where two of its CTAs lay around a small one, the third had no room until one of
+// them ended (16 sequences of up to 128K: 960 us, not 620; selection and decode of one
+// 32K sequence: 19.5 us, not 16.7).
 #pragma once
 
 #include <cuda_bf16.h>
