@@ -108,8 +108,8 @@ int check_workspace(const void* ws, size_t bytes, const PagedLayout& L) {
 
 bool bad_ptr(const void* p, size_t a) { return !p || !aligned(p, a); }
 
-// One pool as {64 elements, rows, d / 64, heads, pages}: a box is one piece of a
-// page of one head, its 64-column halves one after the other, 128-byte swizzle.
+// One pool as {64 elements, rows, d / 64, heads, pages}: a box is 64 columns of a
+// piece of a page of one head, 128-byte swizzle.
 int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
   auto fn = tensor_map_encoder();
   if (!fn) return HYLRA_ERR_CUDA;
@@ -123,8 +123,7 @@ int pool_map(CUtensorMap* tm, const void* base, const hylra_paged_t* s) {
                                  bytes(s->head_stride, s->num_kv_heads),
                                  bytes(s->page_stride, s->num_pages)};
   const int utok = s->head_dim == 128 ? DecodeShape<128>::UTOK : DecodeShape<64>::UTOK;
-  const cuuint32_t box[5] = {64, (cuuint32_t)std::min(s->page_size, utok),
-                             (cuuint32_t)(s->head_dim / 64), 1, 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)std::min(s->page_size, utok), 1, 1, 1};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(
       tm, s->dtype == HYLRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
@@ -174,34 +173,23 @@ int launch(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? HYLRA_OK : HYLRA_ERR_CUDA;
 }
 
-// The decode kernel's ring stages, CTAs per SM and shared memory for a batch:
-// three CTAs with two stages each; where a large batch's lengths do not fit beside
-// them, two with three.
-struct DecodePlan {
-  int nst, ctas;
-  size_t smem;
-};
-template <int HD, typename T>
-DecodePlan decode_plan(int B) {
-  constexpr int SPLIT = Elem<T>::SPLIT;
-  DecodePlan pl{2, kCtasPerSM, 0};
-  auto fits = [&] { return (size_t)pl.ctas * (decode_smem<HD, SPLIT>(pl.nst, B) + 1024) <= kSmemSM; };
-  if (!fits()) pl = DecodePlan{3, 2, 0};
-  if (!fits()) pl.nst = 2;
-  pl.smem = decode_smem<HD, SPLIT>(pl.nst, B);
-  return pl;
-}
-
 template <int HD, typename T, bool LIST>
 int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, DecodeParams& p, int sms,
                   int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
+  constexpr int SPLIT = Elem<T>::SPLIT;
   auto kernel = paged_decode_kernel<HD, T, LIST>;
   if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
-  const DecodePlan pl = decode_plan<HD, T>(p.B);
-  p.nst = pl.nst;
-  const int G = std::min(pl.ctas * sms, MAX_GRID);
-  const size_t smem = pl.smem;
+  // three CTAs to an SM with two stages each; where a large batch's lengths do not
+  // fit beside them, two with three, or (from about 1000 sequences) with two
+  auto fits = [&](int ctas, int nst) {
+    return ctas * (decode_smem<HD, SPLIT>(nst, p.B) + 1024) <= kSmemSM;
+  };
+  const int ctas = fits(kCtasPerSM, 2) ? kCtasPerSM : 2;
+  p.nst = ctas == 2 && fits(2, 3) ? 3 : 2;
+  const size_t smem = decode_smem<HD, SPLIT>(p.nst, p.B);
+  static_assert(2 * (decode_smem<HD, SPLIT>(2, MAX_B) + 1024) <= kSmemSM, "two CTAs to an SM");
+  const int G = std::min(ctas * sms, MAX_GRID);
   if (int rc = launch(kernel, dim3(G), NTHR, smem, stream, 1, tmK, tmV, p)) return rc;
   // fewer heads than CTAs: a CTA per head and 32 float4 columns; else a CTA per
   // decode CTA (at most one head that it holds in part ends after it)
@@ -269,8 +257,6 @@ int launch_select_r(const SelectParams& p, int cs, size_t smem, int nbh, int dev
   static std::atomic<uint64_t> done{0};
   auto kernel = paged_select_kernel<HD, T, R>;
   if (int rc = prepare(kernel, done, dev, kSmemMax)) return rc;
-  // its CTAs start beside the join of a call before: the decode kernel's footprint
-  smem = std::max(smem, decode_plan<HD, T>(p.B).smem);
   return launch(kernel, dim3(cs, nbh), NT_SEL, smem, stream, cs, p);
 }
 

@@ -12,12 +12,10 @@
 // Every kernel is launched as a programmatic dependent and waits for the
 // preceding kernel before its first access to global memory (but for the join's,
 // see there).  Only the decode kernel and the join let their dependents start early.
-// What may then share an SM with decode CTAs that start has the decode kernel's
-// shared memory footprint (the join; the selection, where it needs no more): a decode
-// kernel that started beside smaller CTAs found its SMs' shared memory in pieces, and
-// where two of its CTAs lay around a small one, the third had no room until one of
-// them ended (16 sequences of up to 128K: 960 us, not 620; selection and decode of one
-// 32K sequence: 19.5 us, not 16.7).
+// The join's CTAs have the decode kernel's shared memory footprint: a decode kernel
+// that started beside smaller ones found its SMs' shared memory in pieces, and where
+// two of its CTAs lay around a small one, the third had no room until one of them
+// ended (16 sequences of up to 128K: 960 us, not 620).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -58,6 +56,10 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float value(uint16_t b) {
     return __uint_as_float((uint32_t)b << 16);
   }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
   static __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0,
                                              uint32_t b1) {
     mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
@@ -73,6 +75,13 @@ struct Elem<__half> {
   }
   static __device__ __forceinline__ float value(uint16_t b) {
     return __half2float(__ushort_as_half(b));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
   }
   static __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0,
                                              uint32_t b1) {
@@ -120,14 +129,15 @@ struct DecodeShape {
   static constexpr int UTOK_LOG2 = HD == 128 ? 6 : 7;
   static constexpr int TT = UTOK / (16 * NWC);
   static constexpr int DT = HD / (16 * NWC);
-  static constexpr int PPITCH = UTOK + 8;   // elements per row of P: rows 4 banks apart
+  static constexpr int HALVES = HD / 64;        // 64-column boxes of a row
+  static constexpr int HALF_BYTES = UTOK * 128; // one half of all rows: [token][128 bytes]
   static constexpr int SLOT = GRP * HD + 2 * GRP;  // partial: O, m, Z
 };
 
 template <int HD, int SPLIT>
 struct DecodeSmem {
   using S = DecodeShape<HD>;
-  uint16_t P[SPLIT][GRP][S::PPITCH];  // weights of the unit's tokens, split into terms
+  alignas(16) uint16_t P[SPLIT][S::UTOK][GRP];  // the tokens' weights, split into terms
   float mx[GRP][NWC];                 // each warp's largest logit
   float zs[NWC][GRP];
   int nv[MAX_STAGES][MAX_PIECES];     // valid rows of each piece of the unit
@@ -324,15 +334,19 @@ __global__ void __launch_bounds__(NTHR, 4)
     if (__any_sync(0xffffffffu, *abort_flag)) return;
     const int k = (i / NWC) & (UB - 1);
     if (k == 0) fetch(i);
-    const int src = (k << ppl) + (lane & (ppu - 1));
+    // lanes 0..15 the boxes of K, 16..31 those of V: a box is 64 columns of a piece
+    const int box = lane & 15, piece = box / S::HALVES, half = box % S::HALVES;
+    const bool mine = piece < ppu;
+    const int src = (k << ppl) + (mine ? piece : 0);
     const int pg = __shfl_sync(0xffffffffu, f_page, src);
     const int rw = __shfl_sync(0xffffffffu, f_rows, src);
     const int r0 = __shfl_sync(0xffffffffu, f_row, src);
     const int b = __shfl_sync(0xffffffffu, f_b, k << ppl);
     const int h = __shfl_sync(0xffffffffu, f_h, k << ppl);
     const int start = __shfl_sync(0xffffffffu, f_start, k << ppl);
-    const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rw > 0));
-    if (lane < MAX_PIECES) sm.nv[s][lane] = lane < ppu ? rw : 0;
+    const bool lead = lane < 16 && half == 0 && piece < MAX_PIECES;  // a lane per piece
+    const uint32_t np = __popc(__ballot_sync(0xffffffffu, lead && mine && rw > 0));
+    if (lead) sm.nv[s][piece] = mine ? rw : 0;
     __syncwarp();
     if (lane == 0) {
       const uint32_t qbytes = start ? (uint32_t)(p.r * HD * 2) : 0u;
@@ -347,10 +361,10 @@ __global__ void __launch_bounds__(NTHR, 4)
                   qbytes, &sm.fullK[s]);
     }
     __syncwarp();
-    const int at = lane & 15;  // lanes 0..15 the K pieces, 16..31 the V pieces
-    if (at < ppu && rw > 0) {
-      uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + at * piece_bytes;
-      tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, 0, h, pg,
+    if (mine && rw > 0) {
+      uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + half * S::HALF_BYTES +
+                     (piece << (brl + 7));
+      tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, half, h, pg,
                   lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
     }
   };
@@ -359,16 +373,21 @@ __global__ void __launch_bounds__(NTHR, 4)
 
   const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
   const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
-  const uint32_t half_bytes = 128u << brl;  // 64 columns of a piece
-  auto tok_base = [&](int t) {  // offset of token t's row (t a multiple of 16) in K or V
-    return (uint32_t)(t >> brl) * piece_bytes + (uint32_t)(t & ((1 << brl) - 1)) * 128u;
-  };
   const int tw = cw * 16 * TT;  // first token of this warp
-  const uint32_t krow = (uint32_t)(xr + (mi & 1) * 8) * 128u;
-  const int kchi = mi >> 1;
-  const uint32_t vrow = (uint32_t)(xr + (mi >> 1) * 8) * 128u;
+  // This lane's ldmatrix rows in K and V.  A 128-byte row holds its 16-byte chunk
+  // ch at place ch ^ (row & 7); row & 7 is xr for every row that the lane reads,
+  // and K's chunks 2 kt + (mi >> 1) are this base's with bits 5 and 6 flipped.
+  const uint32_t kofs = (uint32_t)(tw + xr + (mi & 1) * 8) * 128u + (uint32_t)(((mi >> 1) ^ xr) << 4);
+  uint32_t vofs[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) {
+    const int ch = 2 * (cw * DT + t) + (mi & 1);
+    vofs[t] = (uint32_t)HALF + (uint32_t)(xr + (mi >> 1) * 8) * 128u +
+              (uint32_t)(ch >> 3) * S::HALF_BYTES + (uint32_t)(((ch & 7) ^ xr) << 4);
+  }
   const float sl = p.scale_log2;
-  const uint32_t pb = smem_u32(&sm.P[0][0][0]) + (uint32_t)xr * (S::PPITCH * 2) + (uint32_t)mi * 16u;
+  const uint32_t pofs = smem_u32(&sm.P[0][0][0]) + (uint32_t)(mi * 8 + xr) * 16u;
+  uint32_t* const pst = reinterpret_cast<uint32_t*>(&sm.P[0][tw + g4][h0]);
 
   uint32_t qf[HD / 16][2];
   float o[DT][4];
@@ -384,10 +403,12 @@ __global__ void __launch_bounds__(NTHR, 4)
     uint8_t* stage = ring + s * STAGE_BYTES;
     mbar_wait_bounded(&sm.fullK[s], ph, abort_flag, p.wait_limit);
     int nvw[TT];  // valid tokens of each 16
+    bool ragged = false;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       const int tok = tw + 16 * t;
       nvw[t] = min(16, max(0, sm.nv[s][tok >> brl] - (tok & ((1 << brl) - 1))));
+      ragged |= nvw[t] < 16;
     }
     if (seg_start) {
       has_start = x.j == 0;
@@ -409,18 +430,23 @@ __global__ void __launch_bounds__(NTHR, 4)
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t kb = smem_u32(stage) + tok_base(tw + 16 * t) + krow;
+      const uint32_t kb = smem_u32(stage) + kofs + (uint32_t)t * 2048u;
 #pragma unroll
       for (int kt = 0; kt < HD / 16; ++kt) {
-        const int ch = 2 * kt + kchi;
         uint32_t f[4];
-        ldsm_x4(kb + (uint32_t)(ch >> 3) * half_bytes + (uint32_t)(((ch & 7) ^ xr) << 4), f[0],
-                f[1], f[2], f[3]);
+        ldsm_x4((kb ^ (uint32_t)((kt & 3) << 5)) + (uint32_t)(kt >> 2) * S::HALF_BYTES, f[0], f[1],
+                f[2], f[3]);
         E::mma((kt & 1) ? a1 : a0, f, qf[kt][0], qf[kt][1]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        a[t][e] = g4 + ((e & 2) ? 8 : 0) < nvw[t] ? a0[e] + a1[e] : -INFINITY;
+      for (int e = 0; e < 4; ++e) a[t][e] = a0[e] + a1[e];
+    }
+    if (ragged) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g4 + ((e & 2) ? 8 : 0) >= nvw[t]) a[t][e] = -INFINITY;
     }
     // the unit's largest logit per head, over all warps
     float mx[2] = {-INFINITY, -INFINITY};
@@ -445,18 +471,23 @@ __global__ void __launch_bounds__(NTHR, 4)
       m_new[e] = fmaxf(m_run[e], fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)) * sl);
       sub[e] = m_new[e] == -INFINITY ? 0.f : m_new[e];  // nothing attended to yet: weights 0
     }
-    // weights relative to the running maximum, each split into 16-bit terms
+    // weights relative to the running maximum, split into 16-bit terms: both heads
+    // of a token in one word
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float w = ex2_approx(fmaf(a[t][e], sl, -sub[e & 1])) * E::SCALE;
-        sum[e & 1] += w;
+      for (int e = 0; e < 4; e += 2) {
+        float w0 = ex2_approx(fmaf(a[t][e], sl, -sub[0])) * E::SCALE;
+        float w1 = ex2_approx(fmaf(a[t][e + 1], sl, -sub[1])) * E::SCALE;
+        sum[0] += w0;
+        sum[1] += w1;
 #pragma unroll
         for (int u = 0; u < E::SPLIT; ++u) {
-          const uint16_t hb = E::bits(w);
-          sm.P[u][(e & 1) ? h1 : h0][tw + 16 * t + g4 + ((e & 2) ? 8 : 0)] = hb;
-          w -= E::value(hb);
+          const uint32_t both = E::pack(w0, w1);
+          pst[(u * UTOK + 16 * t + 4 * e) * (GRP / 2)] = both;
+          const float2 v = E::unpack(both);
+          w0 -= v.x;
+          w1 -= v.y;
         }
       }
     if (m_new[0] != m_run[0] || m_new[1] != m_run[1]) {
@@ -475,21 +506,18 @@ __global__ void __launch_bounds__(NTHR, 4)
     z_run[0] += sum[0];
     z_run[1] += sum[1];
     mbar_wait_bounded(&sm.fullV[s], ph, abort_flag, p.wait_limit);
-    bool ragged = false;
-#pragma unroll
-    for (int t = 0; t < TT; ++t) ragged |= nvw[t] < 16;
     if (ragged) {
       // rows past the end, or of pages that were not loaded, may hold anything
       // (NaN included): zero weights need zero values
       constexpr int CH = HD / 8;  // 16-byte chunks per row
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        uint8_t* rows = stage + HALF + tok_base(tw + 16 * t);
+        uint8_t* rows = stage + HALF + (tw + 16 * t) * 128;
         for (int idx = lane; idx < 16 * CH; idx += 32) {
           const int row = idx / CH, ch = idx % CH;
           if (row >= nvw[t])
-            *reinterpret_cast<uint4*>(rows + (ch >> 3) * half_bytes + row * 128 + (ch & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(rows + (ch >> 3) * S::HALF_BYTES + row * 128 +
+                                      (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
       fence_proxy_async_smem();
@@ -503,23 +531,21 @@ __global__ void __launch_bounds__(NTHR, 4)
       for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[u][t][e] = 0.f;
-    const uint32_t vb = smem_u32(stage) + HALF + vrow;
+    const uint32_t vb = smem_u32(stage);
 #pragma unroll
     for (int c2 = 0; c2 < UTOK / 32; ++c2) {
       uint32_t pf[E::SPLIT][4];  // 32 tokens' B fragments of each term
 #pragma unroll
       for (int u = 0; u < E::SPLIT; ++u)
-        ldsm_x4(pb + (uint32_t)u * (GRP * S::PPITCH * 2) + (uint32_t)c2 * 64u, pf[u][0], pf[u][1],
-                pf[u][2], pf[u][3]);
+        ldsm_x4_trans(pofs + (uint32_t)(u * UTOK + c2 * 32) * 16u, pf[u][0], pf[u][1], pf[u][2],
+                      pf[u][3]);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
-          const int ch = 2 * (cw * DT + t) + (mi & 1);
           uint32_t vf[4];
-          ldsm_x4_trans(vb + tok_base(c2 * 32 + c * 16) + (uint32_t)(ch >> 3) * half_bytes +
-                            (uint32_t)(((ch & 7) ^ xr) << 4),
-                        vf[0], vf[1], vf[2], vf[3]);
+          ldsm_x4_trans(vb + vofs[t] + (uint32_t)(c2 * 32 + c * 16) * 128u, vf[0], vf[1], vf[2],
+                        vf[3]);
 #pragma unroll
           for (int u = 0; u < E::SPLIT; ++u) E::mma(acc[u][t], vf, pf[u][2 * c], pf[u][2 * c + 1]);
         }
