@@ -363,8 +363,8 @@ typedef struct hylra_paged {
   int32_t max_pages;    /* columns of block_table; max_pages * page_size <=
                            HYLRA_MAX_SEQLEN                                            */
   int64_t page_stride;  /* strides in elements: multiples of 8, below 2^39;            */
-  int64_t head_stride;  /*   rows of d elements must not overlap                       */
-  int64_t token_stride;
+  int64_t head_stride;  /*   rows of d elements must not overlap (the stride of a      */
+  int64_t token_stride; /*   dimension of extent 1 is not used)                        */
   float softmax_scale;  /* logit scale; 0: 1/sqrt(d).  Finite, >= 0                    */
 } hylra_paged_t;
 
@@ -425,7 +425,9 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
  * q: [B][Hq][d]; out: fp32 [B][Hq][d]; lse: fp32 [B][Hq] or NULL, the natural
  * logarithm of the softmax denominator (sum of exp of the scaled logits), with
  * which outputs over disjoint parts of a sequence can be joined.  A sequence
- * without tokens gets zeros and -inf. */
+ * without tokens gets zeros and -inf.  Attending to a non-finite value makes the
+ * outputs of its KV head non-finite.  Results do not depend on the order in
+ * which the GPU runs the call's parts: equal inputs give equal bits. */
 int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,
                        const void* V_pages, const int32_t* block_table, const int32_t* seqlens,
                        float* out, float* lse, void* workspace, size_t workspace_bytes,

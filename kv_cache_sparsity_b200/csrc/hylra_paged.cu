@@ -87,6 +87,7 @@ int check_pool(const hylra_paged_t* s) {
               {s->head_stride, s->num_kv_heads},
               {s->page_stride, s->num_pages}};
   for (const Dim& x : dim) {
+    if (x.extent == 1) continue;  // never used
     if (x.stride < 0 || x.stride % 8 != 0) return HYLRA_ERR_INVALID;
     if (x.stride >= (int64_t(1) << 39)) return HYLRA_ERR_UNSUPPORTED;
   }

@@ -204,6 +204,13 @@ def test_append_lengths(tokens, hkv):
         assert check_append(append_case(held, [1] * tokens, 64, hkv=hkv, seed=tokens), 64) == 0
 
 
+@pytest.mark.parametrize("hkv,d", [(1, 64), (3, 64), (3, 128), (11, 128), (40, 64)])
+def test_append_heads(hkv, d):
+    """Fewer and more columns than a CTA takes, and K and V meeting inside one."""
+    case = append_case([3, 0, 31], [40, 70, 1], 32, hkv=hkv, d=d, dtype="fp16", seed=hkv)
+    assert check_append(case, 32) == 0
+
+
 def test_append_skips_slots():
     case = append_case([0, 3], [40, 20], 16)
     slots = list(case[6])
@@ -272,6 +279,31 @@ def test_decode_split_and_join(lens, hq, hkv, d, dtype):
 def test_decode_many_short_sequences():
     lens = tuple(int(x) for x in np.random.default_rng(1).integers(0, 300, 1024))
     c = T.make_cache(lens, 16, 4, 2, 64, "bf16", seed=1)
+    T.check_attention(c, c.decode(), oracle_decode(c))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("batch,d,dtype", [(400, 64, "bf16"), (500, 128, "fp16"),
+                                           (900, 128, "bf16"), (1000, 64, "fp16"),
+                                           (1024, 128, "bf16")])
+def test_decode_batch_sizes(batch, d, dtype):
+    """Batches whose lengths leave room for fewer CTAs per SM, or for fewer stages."""
+    lens = tuple(int(x) for x in np.random.default_rng(batch).integers(0, 100, batch))
+    c = T.make_cache(lens, 16, 2, 1, d, dtype, seed=batch)
+    T.check_attention(c, c.decode(), oracle_decode(c))
+    lists = np.random.default_rng(0).integers(0, 3, (batch, 1, 3))
+    lists = np.where(lists < np.array([O.pages_of(n, 16) for n in lens])[:, None, None], lists, -1)
+    T.check_attention(c, c.decode_topk(i32(lists.tolist())), oracle_decode(c, lists))
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_decode_single_page_pool_and_single_head(page):
+    """Dimensions of one element, whose strides mean nothing."""
+    c = T.make_cache((page - 3,), page, 4, 1, 128, "bf16", seed=page, spare=0)
+    c.keys = c.keys.as_strided(c.keys.shape, (1, 3, 128, 1))
+    c.vals = c.vals.as_strided(c.vals.shape, (7, 5, 128, 1))
+    c.shape = H.make_paged_shape(1, 4, 1, page, 1, 1, pool=c.keys)
     T.check_attention(c, c.decode(), oracle_decode(c))
     assert c.status() == 0
 
@@ -652,6 +684,42 @@ def test_calls_of_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_calls_in_a_row_without_waiting_for_any():
+    """Each call starts beside the end of the one before it, of every other kind."""
+    a = T.make_cache((9000, 40), 64, 8, 2, 128, "bf16", seed=30)
+    b = T.make_cache((700,) * 30, 16, 8, 2, 64, "fp16", seed=31)
+    r = Requests(list(range(60)), [1] * 60, 16, seed=5)
+    means = make_means(a), make_means(b)
+    dense = torch.randn(2, 1, 2, 640, 128, device="cuda").bfloat16()
+    dshape = H.make_shape(1, 8, 2, 3, 640, kv_capacity=640)
+    dws = torch.empty(H.workspace_bytes(dshape), dtype=torch.uint8, device="cuda")
+    H.workspace_init(dws)
+
+    def everything():
+        got = []
+        for c, m in ((a, means[0]), (b, means[1])):
+            idx = torch.empty(len(c.lens), c.hkv, 5, dtype=torch.int32, device="cuda")
+            got += [*c.decode(), idx]
+            H.paged_select(c.shape, c.q, m, c.table, c.seqlens, idx, c.ws)
+            got += c.decode_topk(idx)
+            out = torch.empty(1, 8, 128, device="cuda")
+            tk = torch.empty(1, 2, 3, dtype=torch.int32, device="cuda")
+            H.decode_full(dshape, a.q[:1].contiguous(), dense[0], dense[1], i32([640]), out, tk,
+                          dws)
+            got += [out, tk, *c.decode()]
+        return got
+
+    want = everything()
+    r.check()
+    torch.cuda.synchronize()
+    rounds = [everything() for _ in range(25)]
+    torch.cuda.synchronize()
+    for got in rounds:
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    assert a.status() == 0 and b.status() == 0
 
 
 def test_one_workspace_serves_every_shape():

@@ -79,6 +79,8 @@ POOL = {"append", "decode", "topk"}
     (dict(page_stride=4096 - 8), INVALID, POOL), (dict(token_stride=120), INVALID, POOL),
     (dict(token_stride=132), INVALID, POOL), (dict(head_stride=0), INVALID, POOL),
     (dict(page_stride=-4096), INVALID, POOL), (dict(page_stride=1 << 39), UNSUPPORTED, POOL),
+    (dict(page_stride=0), INVALID, POOL), (dict(num_pages=1 << 20, page_stride=1 << 30),
+                                           UNSUPPORTED, POOL),
 ])
 def test_shapes_refused(lib, kw, code, who):
     s = _shape(**kw)
