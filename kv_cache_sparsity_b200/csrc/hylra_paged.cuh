@@ -164,28 +164,38 @@ struct Unit {
   int b, h, j, U;  // part j of the U units of (b, h)
 };
 
-__device__ __forceinline__ Unit locate(const int* prefix, int B, int Hkv, int u) {
+// Units are ordered (sequence, KV head, part); up[b]: the units of one head of
+// sequences 0 .. b-1, so that sequence b's begin at up[b] * Hkv.
+__device__ __forceinline__ Unit locate(const int* up, int B, int Hkv, int u) {
   int lo = 0, hi = B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
+    if (up[mid] * Hkv <= u) lo = mid; else hi = mid - 1;
   }
   Unit x;
   x.b = lo;
-  x.U = (prefix[lo + 1] - prefix[lo]) / Hkv;
-  const int off = u - prefix[lo];
-  x.h = off / x.U;
+  x.U = up[lo + 1] - up[lo];
+  const int off = u - up[lo] * Hkv;
+  // off / U by an fp32 quotient, which is off by one at most
+  x.h = (int)(__fdividef((float)off, (float)x.U));
   x.j = off - x.h * x.U;
+  if (x.j < 0) {
+    --x.h;
+    x.j += x.U;
+  } else if (x.j >= x.U) {
+    ++x.h;
+    x.j -= x.U;
+  }
   return x;
 }
 
-__device__ __forceinline__ void advance(const int* prefix, int B, int Hkv, Unit& x) {
+__device__ __forceinline__ void advance(const int* up, int B, int Hkv, Unit& x) {
   if (++x.j < x.U) return;
   x.j = 0;
   if (++x.h < Hkv) return;
   x.h = 0;
-  do { ++x.b; } while (x.b < B && prefix[x.b + 1] == prefix[x.b]);
-  if (x.b < B) x.U = (prefix[x.b + 1] - prefix[x.b]) / Hkv;
+  do { ++x.b; } while (x.b < B && up[x.b + 1] == up[x.b]);
+  if (x.b < B) x.U = up[x.b + 1] - up[x.b];
 }
 
 // CTA that holds unit u when CTA c holds [floor(c*T/G), floor((c+1)*T/G)), G <= T.
@@ -202,10 +212,10 @@ __device__ __forceinline__ int checked_len(const int32_t* seqlens, int b, int ca
   return 0;
 }
 
-// prefix[b + 1]: units of sequence b times Hkv, by all threads; then their
-// running sum, by warp 0.
+// up[b + 1]: units of a head of sequence b, by all threads; then their running sum,
+// by warp 0.
 template <bool LIST, int UTOK>
-__device__ __forceinline__ void count_units(const DecodeParams& p, int* prefix, int* lens,
+__device__ __forceinline__ void count_units(const DecodeParams& p, int* up, int* lens,
                                             bool report) {
   const int psl = p.ps_log2;
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
@@ -213,24 +223,24 @@ __device__ __forceinline__ void count_units(const DecodeParams& p, int* prefix, 
     const int nb = (n + (1 << psl) - 1) >> psl;
     const int tokens = LIST ? min(p.k, nb) << psl : n;
     if (lens) lens[b] = n;
-    prefix[b + 1] = ((tokens + UTOK - 1) / UTOK) * p.Hkv;
+    up[b + 1] = (tokens + UTOK - 1) / UTOK;
   }
 }
-__device__ __forceinline__ void sum_units(const DecodeParams& p, int* prefix) {
+__device__ __forceinline__ void sum_units(const DecodeParams& p, int* up) {
   const int lane = threadIdx.x;
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
+    int v = b0 + lane < p.B ? up[b0 + lane + 1] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, v, off);
       if (lane >= off) v += o;
     }
     v += carry;
-    if (b0 + lane < p.B) prefix[b0 + lane + 1] = v;
+    if (b0 + lane < p.B) up[b0 + lane + 1] = v;
     carry = __shfl_sync(0xffffffffu, v, 31);
   }
-  if (lane == 0) prefix[0] = 0;
+  if (lane == 0) up[0] = 0;
 }
 
 template <int HD, typename T, bool LIST>
@@ -247,8 +257,8 @@ __global__ void __launch_bounds__(NTHR, 4)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int nst = p.nst;
   Smem& sm = *reinterpret_cast<Smem*>(ring + nst * STAGE_BYTES);
-  int* prefix = reinterpret_cast<int*>(ring + nst * STAGE_BYTES + decode_fixed<HD, E::SPLIT>(nst));
-  int* lens = prefix + p.B + 1;  // prefix[b]: units before sequence b, of all heads
+  int* up = reinterpret_cast<int*>(ring + nst * STAGE_BYTES + decode_fixed<HD, E::SPLIT>(nst));
+  int* lens = up + p.B + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == NTHR - 1) {
     for (int s = 0; s < nst; ++s) {
@@ -269,11 +279,11 @@ __global__ void __launch_bounds__(NTHR, 4)
   griddep_wait();
   griddep_launch_dependents();
 
-  count_units<LIST, UTOK>(p, prefix, lens, blockIdx.x == 0);
+  count_units<LIST, UTOK>(p, up, lens, blockIdx.x == 0);
   __syncthreads();
-  if (warp == 0) sum_units(p, prefix);
+  if (warp == 0) sum_units(p, up);
   __syncthreads();
-  const int total = prefix[p.B];
+  const int total = up[p.B] * p.Hkv;
   const int G = total > 0 ? min((int)gridDim.x, total) : 1;
   const bool works = (int)blockIdx.x < G && total > 0;
   const int lo = works ? (int)((long long)blockIdx.x * total / G) : 0;
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(NTHR, 4)
   const int cw = warp;
   // sequences without units: zeros and -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (prefix[b + 1] != prefix[b]) continue;
+    if (up[b + 1] != up[b]) continue;
     for (int i = tid; i < p.Hq * HD; i += NTHR) p.out[(size_t)b * p.Hq * HD + i] = 0.f;
     if (p.lse)
       for (int i = tid; i < p.Hq; i += NTHR) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
@@ -303,7 +313,7 @@ __global__ void __launch_bounds__(NTHR, 4)
     f_rows = f_start = 0;
     const int ui = base + NWC * (lane >> ppl);
     if (ui >= n) return;
-    const Unit x = locate(prefix, p.B, p.Hkv, lo + ui);
+    const Unit x = locate(up, p.B, p.Hkv, lo + ui);
     f_b = x.b;
     f_h = x.h;
     f_start = ui == 0 || x.j == 0;
@@ -392,7 +402,7 @@ __global__ void __launch_bounds__(NTHR, 4)
   uint32_t qf[HD / 16][2];
   float o[DT][4];
   float m_run[2], z_run[2];
-  Unit x = locate(prefix, p.B, p.Hkv, lo);
+  Unit x = locate(up, p.B, p.Hkv, lo);
   bool has_start = false;  // this CTA holds the segment's first unit
   int s = 0;
   uint32_t ph = 0;
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(NTHR, 4)
         }
       }
     }
-    advance(prefix, p.B, p.Hkv, x);
+    advance(up, p.B, p.Hkv, x);
   }
   __syncthreads();
   if (*abort_flag && tid == 0) {
@@ -648,7 +658,7 @@ __global__ void __launch_bounds__(NT_JOIN)
     paged_join_kernel(const __grid_constant__ DecodeParams p, int grid_decode, int by_head) {
   using S = DecodeShape<HD>;
   constexpr int NG = NT_JOIN / 32, CB = 8;
-  extern __shared__ int prefix[];  // [B + 1]
+  extern __shared__ int up[];  // [B + 1]
   __shared__ float4 wacc[NG][32];
   __shared__ float wm[NG][32], wz[NG][32];
   static_assert(sizeof(wacc) + sizeof(wm) + sizeof(wz) == JOIN_STATIC, "join footprint");
@@ -656,17 +666,17 @@ __global__ void __launch_bounds__(NT_JOIN)
   griddep_launch_dependents();
   // Lengths are older than the decode kernel, which has waited for everything
   // before it: they are read ahead of the wait.
-  count_units<LIST, S::UTOK>(p, prefix, nullptr, false);
+  count_units<LIST, S::UTOK>(p, up, nullptr, false);
   __syncthreads();
-  if (warp == 0) sum_units(p, prefix);
+  if (warp == 0) sum_units(p, up);
   __syncthreads();
-  const int total = prefix[p.B], G = min(grid_decode, max(total, 1));
+  const int total = up[p.B] * p.Hkv, G = min(grid_decode, max(total, 1));
   int bh = 0, first = 0, nc = 0;
   if (by_head) {
     bh = (int)blockIdx.x;
-    const int b = bh / p.Hkv, U = (prefix[b + 1] - prefix[b]) / p.Hkv;
+    const int b = bh / p.Hkv, U = up[b + 1] - up[b];
     if (U > 0) {
-      const int start = prefix[b] + (bh - b * p.Hkv) * U;
+      const int start = up[b] * p.Hkv + (bh - b * p.Hkv) * U;
       first = unit_owner(start, total, G);
       nc = unit_owner((long long)start + U - 1, total, G) - first + 1;
     }
@@ -674,7 +684,7 @@ __global__ void __launch_bounds__(NT_JOIN)
     first = (int)blockIdx.x;
     const int lo = (int)((long long)first * total / G);
     const int end = (int)((long long)(first + 1) * total / G) - 1;
-    const Unit x = locate(prefix, p.B, p.Hkv, end);
+    const Unit x = locate(up, p.B, p.Hkv, end);
     bh = x.b * p.Hkv + x.h;
     if (end - x.j >= lo) nc = unit_owner((long long)end - x.j + x.U - 1, total, G) - first + 1;
   }
