@@ -34,6 +34,38 @@ constexpr int MAX_PAGE = 128;         // tokens per page
 constexpr int MAX_GRID = 512;         // CTAs of the decode kernel
 constexpr int MAX_B = HYLRA_MAX_BATCH;
 
+// -------------------------------------------------------- device primitives
+
+// 5-D tiled TMA load (box given by the tensor map) into shared memory, completion
+// counted in bytes on an mbarrier.  x must be a multiple of 16 bytes / element size.
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* tm, int x, int y, int z,
+                                            int u, int v, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v),
+      "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// D(16x8, f32) += A(16x16, fp16, row) * B(16x8, fp16, col)
+__device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Stores to the shared memory of another CTA of the cluster (address from mapa).
+__device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
 // ------------------------------------------------------------ element types
 
 template <typename T>
