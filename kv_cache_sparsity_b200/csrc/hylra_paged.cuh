@@ -130,7 +130,7 @@ struct Elem<__half> {
 constexpr int NWC = 4;
 constexpr int NTHR = NWC * 32;
 constexpr int MAX_PIECES = 8;            // pieces per unit: 128 tokens of 16-token pages
-constexpr int MAX_STAGES = 4;
+constexpr int MAX_STAGES = 3;
 constexpr int STAGE_BYTES = 32768;       // K and V of one unit
 
 struct DecodeParams {
@@ -177,7 +177,7 @@ struct DecodeSmem {
   alignas(8) uint64_t fullV[MAX_STAGES];
   alignas(8) uint64_t empty[MAX_STAGES];
   int abort;
-  int issued;                         // units requested so far
+  int issued[MAX_STAGES];             // requests into each stage so far
   alignas(16) uint8_t qslot[MAX_STAGES][GRP * HD * 2];  // the first nst are used
 };
 
@@ -275,6 +275,20 @@ __device__ __forceinline__ void sum_units(const DecodeParams& p, int* up) {
   if (lane == 0) up[0] = 0;
 }
 
+// S^T = K Q^T and O^T = V^T P^T on the 16-bit matrix units (M: tokens or dims, N: the
+// r <= 8 heads), softmax online in base 2.  One query row per head makes this a
+// matrix-vector product: 4 r operations a byte, against 250 that the tensor cores
+// could do in the time of a byte from memory; a tcgen05 tile (M of 64 or more, N the
+// heads) would be as empty and need its accumulators moved to registers for the
+// softmax, so the warps' own matrix instructions are used (16 % of their rate).
+// Bound by memory: each key and value is read once.  16 sequences of up to 128K, 8 KV
+// heads, d 128: 620 us back to back, 6.8 TB/s; one of 32K: 30 us, of which about 4 are
+// the way to the first data and 5 the last CTAs and the join.  Three CTAs of four warps
+// and two 32 KB stages to an SM: one CTA of nine warps with three 64 KB stages waited
+// for its own arithmetic (697 us; a unit's chain of steps takes 1 us whatever its size),
+// two CTAs with three stages each take 650 us.  A common maximum first, one barrier
+// more than weights relative to each warp's own, costs nothing and saves a rescaling
+// path.
 template <int HD, typename T, bool LIST>
 __global__ void __launch_bounds__(NTHR, 4)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(NTHR, 4)
       mbar_init(&sm.empty[s], NWC);
     }
     sm.abort = 0;
-    sm.issued = 0;
+    for (int s = 0; s < MAX_STAGES; ++s) sm.issued[s] = 0;
     fence_mbar_init();
   }
   if (tid == 0) {
@@ -393,7 +407,7 @@ __global__ void __launch_bounds__(NTHR, 4)
     if (lane == 0) {
       const uint32_t qbytes = start ? (uint32_t)(p.r * HD * 2) : 0u;
       const uint32_t bytes = np * piece_bytes, bytesK = bytes + qbytes;
-      sm.issued = i + 1;
+      ++sm.issued[s];
       if (bytesK) mbar_arrive_expect_tx(&sm.fullK[s], bytesK); else mbar_arrive(&sm.fullK[s]);
       if (bytes) mbar_arrive_expect_tx(&sm.fullV[s], bytes); else mbar_arrive(&sm.fullV[s]);
       if (start)
@@ -410,7 +424,7 @@ __global__ void __launch_bounds__(NTHR, 4)
                   lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
     }
   };
-  for (int i = 0; i < nst && i < n; ++i)  // nst <= 4: a different warp each
+  for (int i = 0; i < nst && i < n; ++i)  // nst <= 3: a different warp each
     if (i == cw) issue(i, i);
 
   const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
@@ -664,9 +678,9 @@ __global__ void __launch_bounds__(NTHR, 4)
   __syncthreads();
   if (*abort_flag && tid == 0) {
     // never exit with a copy into this CTA's shared memory in flight
-    const int issued = sm.issued;
-    for (int t = 0; t < nst && t < issued; ++t) {
-      const uint32_t lp = (uint32_t)(((issued - 1 - t) / nst) & 1);  // last phase of stage t
+    for (int t = 0; t < nst; ++t) {
+      if (sm.issued[t] == 0) continue;
+      const uint32_t lp = (uint32_t)(sm.issued[t] - 1) & 1u;  // the stage's last phase
       mbar_drain(&sm.fullK[t], lp);
       mbar_drain(&sm.fullV[t], lp);
     }
@@ -677,9 +691,9 @@ __global__ void __launch_bounds__(NTHR, 4)
 // Joins by log-sum-exp the heads whose units several CTAs hold.  Grid (heads or
 // decode CTAs, column parts): with by_head, x is a (sequence, KV head); else it
 // is a decode CTA, for the head that begins in it and ends in a later one (at
-// most one).  A warp takes every fourth contributor, a lane one float4 column;
-// all of a warp's loads of 64 contributors go out together, so that a join is
-// one trip to L2.  It replaced a join by the last CTA to finish a head (a ticket
+// most one).  A warp takes every eighth contributor, a lane one float4 column;
+// the loads of 64 contributors go out together, so that a join is one trip to L2
+// and costs its latency.  It replaced a join by the last CTA to finish a head (a ticket
 // each): one SM then fetched all partials, 7-8 us behind the last unit of one
 // 32K sequence, against about 2.5 us here.
 constexpr int NT_JOIN = 256;
