@@ -20,8 +20,9 @@ namespace {
 
 constexpr size_t kSmemMax = 232448;  // 227 KB of dynamic shared memory per CTA
 constexpr size_t kSmemSM = 233472;   // 228 KB of shared memory per SM, 1 KB of it per CTA reserved
-// the largest table: 16384 pages of 16 tokens over eight CTAs, 8 heads, 1024 of them wanted
-static_assert(sizeof(SelectSmem) + 8 * 1024 * 8 + 2048 * 8 + 8 * 2048 * 8 <= kSmemMax,
+// the largest table: 16384 pages of 16 tokens over eight CTAs, 8 heads
+static_assert(sizeof(SelectSmem) + 8 * 2048 * 8 + 16384 * 4 <= kSmemMax &&
+                  sizeof(SelectSmem) + sizeof(RankSmem) + 16384 * 4 <= kSmemMax,
               "select kernel shared memory");
 constexpr int kCtasPerSM = 3;        // of the decode kernel, at most
 
@@ -429,11 +430,11 @@ int hylra_paged_select(const hylra_paged_t* shape, const void* q, const void* ke
   p.scale = shape->softmax_scale > 0.f ? (double)shape->softmax_scale
                                        : 1.0 / std::sqrt((double)shape->head_dim);
   // CTAs per (sequence, KV head): as many as run at once, two to an SM, and more
-  // where a CTA would have over 1024 pages to sort (eight have 2048 at most)
+  // where a CTA would hold the weights of over 1024 pages (eight hold 2048 at most)
   int cs = 1;
   while (cs < MAX_CS && (nbh * cs * 2 <= 2LL * sms || (p.max_pages + cs - 1) / cs > 1024)) cs *= 2;
   p.ppc = (p.max_pages + cs - 1) / cs;
-  const size_t smem = select_smem(p.r, p.ppc, cs, topk);
+  const size_t smem = select_smem(p.r, p.ppc, p.max_pages);
   cudaStream_t st = (cudaStream_t)stream;
   if (shape->head_dim == 128)
     return shape->dtype == HYLRA_BF16

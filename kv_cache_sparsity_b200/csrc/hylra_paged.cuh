@@ -62,8 +62,8 @@ __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1
 __device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
-__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // ------------------------------------------------------------ element types
@@ -831,32 +831,35 @@ struct SelectSmem {
   double wm[NW_SEL][GRP], wz[NW_SEL][GRP];
   double cm[MAX_CS][GRP], cz[MAX_CS][GRP];  // each CTA's maxima and sums, sent by the peers
   double m[GRP], f[GRP];
+  int wsum[NW_SEL];
+  int count, last;
   alignas(16) double q[GRP][4][34];  // a head's four quarters of the dims, 4 banks apart
 };
 
-inline __host__ __device__ int pow2_above(int x) {
-  int p = 1;
-  while (p < x) p <<= 1;
-  return p;
-}
+constexpr int SEL_CAP = 2048;   // entries that one sort takes
+constexpr int SEL_BINS = 4096;  // of the histogram before it
 
-// Dynamic shared memory: SelectSmem, every CTA's best entries (sorted, a power of
-// two of them), this CTA's entries (a multiple of NT_SEL), the weights e[r][ppc].
-inline __host__ __device__ int select_best(int ppc, int k) { return pow2_above(k < ppc ? k : ppc); }
-inline __host__ __device__ int select_entries(int ppc) {
-  return ppc <= NT_SEL ? NT_SEL : pow2_above(ppc);
+// What ranking needs in the place of the weights.
+struct RankSmem {
+  uint64_t list[SEL_CAP], sorted[SEL_CAP];
+  int bins[SEL_BINS];
+};
+
+// Dynamic shared memory: SelectSmem, the weights e[r][ppc] (later RankSmem), and a
+// key per page of the table.
+inline __host__ __device__ size_t select_weights(int r, int ppc) {
+  const size_t e = (size_t)r * ppc * 8;
+  return e > sizeof(RankSmem) ? e : sizeof(RankSmem);
 }
-inline __host__ __device__ size_t select_smem(int r, int ppc, int cs, int k) {
-  return sizeof(SelectSmem) + (size_t)cs * select_best(ppc, k) * 8 +
-         (size_t)select_entries(ppc) * 8 + (size_t)r * ppc * 8;
+inline __host__ __device__ size_t select_smem(int r, int ppc, int max_pages) {
+  return sizeof(SelectSmem) + select_weights(r, ppc) + (size_t)max_pages * 4;
 }
 
 // An fp32 value times 2^-896 as a double, by its bits: the fp32 exponent stands in
 // the double's field as it is, and the query is multiplied by 2^896 instead.
 // Two integer instructions, beside the products (the conversion instruction took
 // as long as they do).  Zeros stay zeros; infinity and NaN must be sorted out by
-// the caller.   x: a 16-bit value's fp32
-// pattern (its last three bits are 0).
+// the caller.  x: a 16-bit value's fp32 pattern (its last three bits are 0).
 __device__ __forceinline__ double widen(uint32_t x) {
   return __hiloint2double((int)((uint32_t)((int)x >> 3) & 0x8fffffffu), 0);
 }
@@ -911,53 +914,140 @@ __device__ __forceinline__ void sort_pass(uint64_t (&v)[N], int lane, int j, int
   }
 }
 
-// In how many of the nl sorted lists' entries (descending, len a power of two,
-// padded with zeros) does an entry exceed v: the lists in lock step, one select
-// per step, no branch.
-template <int NL>
-__device__ __forceinline__ int count_above(const uint64_t* lists, int pitch, int nl, int len,
-                                           uint64_t v) {
-  int pos[NL], sum = 0;
-#pragma unroll
-  for (int t = 0; t < NL; ++t) pos[t] = 0;
-  for (int step = len >> 1; step > 0; step >>= 1)
-#pragma unroll
-    for (int t = 0; t < NL; ++t)
-      if (t < nl) pos[t] += lists[t * pitch + pos[t] + step - 1] > v ? step : 0;
-#pragma unroll
-  for (int t = 0; t < NL; ++t)
-    if (t < nl) sum += pos[t] + (lists[t * pitch + pos[t]] > v ? 1 : 0);
-  return sum;
-}
-
-// Puts list[0..256 N) (distinct entries, zeros at the end) in descending order
-// into sorted, of which only the first `want` places matter.  Each warp sorts
-// 32 N of them in registers; an entry's place is how many entries of the warps'
-// lists exceed it.
+// Puts list[0 .. 256 N) (distinct entries, zeros at the end) in descending order
+// into sorted, of which the first `want` places matter.  Each warp sorts 32 N of
+// them in registers; an entry's place is how many entries of the warps' lists exceed
+// it: binary searches in lock step, a select per step and no branch.
 template <int N>
 __device__ void block_sort(uint64_t* list, uint64_t* sorted, int want) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  constexpr int LEN = 32 * N;
   uint64_t v[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = list[wid * 32 * N + lane * N + i];
+  for (int i = 0; i < N; ++i) v[i] = list[wid * LEN + lane * N + i];
 #pragma unroll 1
-  for (int k = 2; k <= 32 * N; k <<= 1)
+  for (int k = 2; k <= LEN; k <<= 1)
 #pragma unroll 1
     for (int j = k >> 1; j > 0; j >>= 1) sort_pass<N>(v, lane, j, k);
 #pragma unroll
-  for (int i = 0; i < N; ++i) list[wid * 32 * N + lane * N + i] = v[i];
+  for (int i = 0; i < N; ++i) list[wid * LEN + lane * N + i] = v[i];
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < N; ++i) {
     uint64_t x = v[0];
 #pragma unroll
     for (int t = 1; t < N; ++t) x = t == i ? v[t] : x;
-    if (x != 0ull && lane * N + i < want) {
-      const int at = count_above<NW_SEL>(list, 32 * N, NW_SEL, 32 * N, x);
-      if (at < want) sorted[at] = x;
+    if (x == 0ull || lane * N + i >= want) continue;
+    int pos[NW_SEL], at = 0;
+#pragma unroll
+    for (int t = 0; t < NW_SEL; ++t) pos[t] = 0;
+    for (int step = LEN / 2; step > 0; step >>= 1)
+#pragma unroll
+      for (int t = 0; t < NW_SEL; ++t)
+        pos[t] += list[t * LEN + pos[t] + step - 1] > x ? step : 0;
+#pragma unroll
+    for (int t = 0; t < NW_SEL; ++t) at += pos[t] + (list[t * LEN + pos[t]] > x ? 1 : 0);
+    if (at < want) sorted[at] = x;
+  }
+  __syncthreads();
+}
+
+// list[0 .. count) sorted, its first `want` entries into sorted.
+__device__ __forceinline__ void sort_entries(RankSmem& rk, int count, int want) {
+  const int n = count <= 256 ? 256 : count <= 512 ? 512 : count <= 1024 ? 1024 : 2048;
+  for (int i = count + threadIdx.x; i < n; i += NT_SEL) rk.list[i] = 0ull;
+  __syncthreads();
+  switch (n) {
+    case 256: block_sort<1>(rk.list, rk.sorted, want); break;
+    case 512: block_sort<2>(rk.list, rk.sorted, want); break;
+    case 1024: block_sort<4>(rk.list, rk.sorted, want); break;
+    default: block_sort<8>(rk.list, rk.sorted, want); break;
+  }
+}
+
+// An entry compares by score (a non-negative fp32 value's bits), then lower page.
+__device__ __forceinline__ uint64_t rank_entry(uint32_t key, int page) {
+  return (uint64_t)key << 32 | (uint32_t)~(uint32_t)page;
+}
+
+// The kr best of keys[0 .. nc), in order, into rk.sorted.  More keys than one sort
+// takes cheaply go through a histogram of their distance from the largest, 2^15
+// units in the last place (0.4 %) a bin over 16 binades: the bins down to the
+// kr-th key hold kr keys and a few more.  Where those are still too many (equal
+// scores) or the wanted keys lie deeper, batches of keys are sorted in with the
+// best so far.
+__device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, RankSmem& rk) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  if (nc <= 512) {
+    for (int i = tid; i < nc; i += NT_SEL) rk.list[i] = rank_entry(keys[i], i);
+    sort_entries(rk, nc, kr);
+    return;
+  }
+  uint32_t top = 0u;
+  for (int i = tid; i < nc; i += NT_SEL) top = max(top, keys[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) sm.wsum[wid] = (int)top;
+  for (int i = tid; i < SEL_BINS; i += NT_SEL) rk.bins[i] = 0;
+  if (tid == 0) {
+    sm.last = -1;
+    sm.count = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW_SEL; ++w) top = max(top, (uint32_t)sm.wsum[w]);
+  for (int i = tid; i < nc; i += NT_SEL) {
+    const uint32_t bin = (top - keys[i]) >> 15;
+    if (bin < SEL_BINS) atomicAdd(&rk.bins[bin], 1);
+  }
+  __syncthreads();
+  {
+    constexpr int PER = SEL_BINS / NT_SEL;
+    int cnt[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      cnt[i] = rk.bins[tid * PER + i];
+      sum += cnt[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    __syncthreads();  // wsum held the maxima
+    if (lane == 31) sm.wsum[wid] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW_SEL; ++w) incl += w < wid ? sm.wsum[w] : 0;
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      // the bin of the kr-th key: one thread finds it
+      if (run < kr && kr <= run + cnt[i] && run + cnt[i] <= SEL_CAP) sm.last = tid * PER + i;
+      run += cnt[i];
     }
   }
   __syncthreads();
+  const int last = sm.last;
+  if (last >= 0) {
+    for (int i = tid; i < nc; i += NT_SEL) {
+      const uint32_t key = keys[i];
+      if ((top - key) >> 15 <= (uint32_t)last) rk.list[atomicAdd(&sm.count, 1)] = rank_entry(key, i);
+    }
+    __syncthreads();
+    sort_entries(rk, sm.count, kr);
+    return;
+  }
+  int have = 0;  // the best so far, in rk.sorted
+  for (int i0 = 0; i0 < nc; i0 += SEL_CAP / 2) {
+    const int n = min(SEL_CAP / 2, nc - i0);
+    for (int i = tid; i < have; i += NT_SEL) rk.list[i] = rk.sorted[i];
+    for (int i = tid; i < n; i += NT_SEL) rk.list[have + i] = rank_entry(keys[i0 + i], i0 + i);
+    __syncthreads();
+    const int all = have + n;
+    have = min(kr, all);
+    sort_entries(rk, all, have);
+  }
 }
 
 // Grid (cs, B * Hkv), a cluster per (sequence, KV head).  The scores decide
@@ -967,8 +1057,8 @@ __device__ void block_sort(uint64_t* list, uint64_t* sorted, int want) {
 // kernel with many pages is bound by the 64-bit units (r d products a page and
 // head at 64 a clock and SM, about the time that the means' 2 d bytes take from
 // memory at r = 4), one with few by the chain of steps.
-// Each CTA ranks its share of the pages by a sort of (score, page) pairs; an
-// entry's rank among all is the number of entries above it in every CTA's list.
+// The CTAs of a cluster share the pages; once their maxima and sums have been
+// exchanged, they send the scores to the first, which ranks them.
 // R: r rounded up to 4 or 8.
 template <int HD, typename T, int R>
 __global__ void __launch_bounds__(NT_SEL, 2)
@@ -977,10 +1067,9 @@ __global__ void __launch_bounds__(NT_SEL, 2)
   SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_sel);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int cs = (int)gridDim.x, rank = (int)blockIdx.x;
-  const int best = select_best(p.ppc, p.k);  // entries that a CTA may contribute, padded
-  uint64_t* lists = reinterpret_cast<uint64_t*>(smem_sel + sizeof(SelectSmem));  // [cs][best]
-  uint64_t* list = lists + cs * best;
-  double* e = reinterpret_cast<double*>(list + select_entries(p.ppc));  // [r][ppc]
+  double* e = reinterpret_cast<double*>(smem_sel + sizeof(SelectSmem));  // [r][ppc]
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectSmem) +
+                                               select_weights(p.r, p.ppc));  // the first CTA's
   const int bh = (int)blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   cluster_arrive_relaxed();
   griddep_wait();
@@ -1180,45 +1269,25 @@ __global__ void __launch_bounds__(NT_SEL, 2)
     if (lane == rank) sm.f[wid] = m == -INFINITY ? 0.0 : f / Z;
   }
   __syncthreads();
-  const int entries = select_entries(np);
+  const uint32_t kbase = mapa_shared(smem_u32(keys), 0);
   bool odd = false;
-  for (int i = tid; i < entries; i += NT_SEL) {
-    uint64_t v = 0ull;  // below every entry
-    if (i < np) {
-      double s = 0.0;
-      for (int t = 0; t < p.r; ++t) s += e[(size_t)t * p.ppc + i] * sm.f[t];
-      float key = (float)s;
-      if (!(key >= 0.f && key < INFINITY)) {
-        key = 0.f;
-        odd = true;
-      }
-      v = ((uint64_t)__float_as_uint(key) << 32) | (uint32_t)~(uint32_t)(s0 + i);
+  for (int i = tid; i < np; i += NT_SEL) {
+    double sc = 0.0;
+    for (int t = 0; t < p.r; ++t) sc += e[(size_t)t * p.ppc + i] * sm.f[t];
+    float key = (float)sc;
+    if (!(key >= 0.f && key < INFINITY)) {
+      key = 0.f;
+      odd = true;
     }
-    list[i] = v;
+    st_dsmem_u32(kbase + (uint32_t)(s0 + i) * 4u, __float_as_uint(key));
   }
   if (odd) atomicOr(p.status, HYLRA_STATUS_NONFINITE);
-  uint64_t* own = lists + rank * best;
-  for (int i = tid; i < best; i += NT_SEL) own[i] = 0ull;
-  __syncthreads();
-  const int mine = min(kr, np);
-  switch (entries / NT_SEL) {
-    case 1: block_sort<1>(list, own, mine); break;
-    case 2: block_sort<2>(list, own, mine); break;
-    case 4: block_sort<4>(list, own, mine); break;
-    default: block_sort<8>(list, own, mine); break;  // a CTA has 2048 pages at most
-  }
-  if (cs > 1) {
-    for (int i = tid; i < best * cs; i += NT_SEL) {
-      const int peer = i / best, at = i - peer * best;
-      if (peer != rank) st_dsmem_u64(mapa_shared(smem_u32(own + at), peer), own[at]);
-    }
-    cluster_sync_all();
-  }
-  for (int i = tid; i < mine; i += NT_SEL) {
-    const uint64_t v = own[i];
-    const int at = cs > 1 ? count_above<MAX_CS>(lists, best, cs, best, v) : i;
-    if (at < kr) dst[forced + at] = c0 + (int32_t)~(uint32_t)(v & 0xffffffffull);
-  }
+  cluster_sync_all();
+  if (rank != 0) return;
+  RankSmem& rk = *reinterpret_cast<RankSmem*>(e);
+  rank_keys(keys, nc, kr, sm, rk);
+  for (int i = tid; i < kr; i += NT_SEL)
+    dst[forced + i] = c0 + (int32_t)~(uint32_t)(rk.sorted[i] & 0xffffffffull);
 }
 
 // ----------------------------------------------------------------- append

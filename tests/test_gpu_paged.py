@@ -526,6 +526,27 @@ def test_select_ties_take_the_lower_page():
     assert c.status() == 0
 
 
+@pytest.mark.parametrize("n", [513, 1500, 2049, 3000, 5000])
+@pytest.mark.parametrize("k", [3, 300, 1024])
+def test_select_many_equal_and_far_scores(n, k):
+    """More equal scores than one sort takes, and wanted pages far below the best."""
+    c = T.make_cache((16 * (n + 1),), 16, 2, 1, 64, "bf16", seed=n)
+    rows = torch.tensor([int(x) for x in c.table[0, : n + 1]], device="cuda")
+    means = torch.ones(c.keys.shape[0], 1, 64, dtype=torch.bfloat16, device="cuda")
+    assert np.array_equal(run_select(c, means, k, 0, 1)[0, 0],
+                          ([n] + list(range(min(k - 1, n))) + [-1] * k)[:k])
+    # the same with a few better and a few much better pages
+    sign = torch.sign(c.q[0].float().sum(0)).bfloat16()
+    means[rows[5:n:97]] = sign * 1.5
+    means[rows[7:n:301]] = sign * 4
+    assert np.array_equal(run_select(c, means, k, 0, 1), oracle_select(c, means, k, 0, 1))
+    # scores over hundreds of binades
+    far = torch.linspace(-40, 40, n + 1, device="cuda")[torch.randperm(n + 1, device="cuda")]
+    means[rows] = (far[:, None, None] * sign).bfloat16()
+    assert np.array_equal(run_select(c, means, k, 0, 1), oracle_select(c, means, k, 0, 1))
+    assert c.status() == 0
+
+
 def test_select_vanishing_scores():
     """Scores that underflow to zero tie, and still come in order."""
     c = T.make_cache((16 * 300,), 16, 2, 1, 64, "bf16", seed=14, sharp=30.0)
