@@ -831,6 +831,7 @@ struct SelectSmem {
   double wm[NW_SEL][GRP], wz[NW_SEL][GRP];
   double cm[MAX_CS][GRP], cz[MAX_CS][GRP];  // each CTA's maxima and sums, sent by the peers
   double m[GRP], f[GRP];
+  uint32_t top[MAX_CS][NW_SEL];  // in the first CTA: the largest keys of the cluster's warps
   int wsum[NW_SEL];
   int count, last;
   alignas(16) double q[GRP][4][34];  // a head's four quarters of the dims, 4 banks apart
@@ -846,13 +847,13 @@ struct RankSmem {
 };
 
 // Dynamic shared memory: SelectSmem, the weights e[r][ppc] (later RankSmem), and a
-// key per page of the table.
+// key per page of the table, read four at a time.
 inline __host__ __device__ size_t select_weights(int r, int ppc) {
-  const size_t e = (size_t)r * ppc * 8;
+  const size_t e = ((size_t)r * ppc * 8 + 15) / 16 * 16;
   return e > sizeof(RankSmem) ? e : sizeof(RankSmem);
 }
 inline __host__ __device__ size_t select_smem(int r, int ppc, int max_pages) {
-  return sizeof(SelectSmem) + select_weights(r, ppc) + (size_t)max_pages * 4;
+  return sizeof(SelectSmem) + select_weights(r, ppc) + ((size_t)max_pages * 4 + 15) / 16 * 16;
 }
 
 // An fp32 value times 2^-896 as a double, by its bits: the fp32 exponent stands in
@@ -976,7 +977,8 @@ __device__ __forceinline__ uint64_t rank_entry(uint32_t key, int page) {
 // kr-th key hold kr keys and a few more.  Where those are still too many (equal
 // scores) or the wanted keys lie deeper, batches of keys are sorted in with the
 // best so far.
-__device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, RankSmem& rk) {
+__device__ void rank_keys(const uint32_t* keys, int nc, int kr, int cs, SelectSmem& sm,
+                          RankSmem& rk) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (nc <= 512) {
     for (int i = tid; i < nc; i += NT_SEL) rk.list[i] = rank_entry(keys[i], i);
@@ -984,20 +986,27 @@ __device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, 
     return;
   }
   uint32_t top = 0u;
-  for (int i = tid; i < nc; i += NT_SEL) top = max(top, keys[i]);
+  for (int i = lane; i < cs * NW_SEL; i += 32) top = max(top, sm.top[0][i]);
   top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) sm.wsum[wid] = (int)top;
   for (int i = tid; i < SEL_BINS; i += NT_SEL) rk.bins[i] = 0;
   if (tid == 0) {
     sm.last = -1;
     sm.count = 0;
   }
   __syncthreads();
+  // the bins of four keys; SEL_BINS past the last key
+  auto bins4 = [&](int i, uint32_t (&key)[4], uint32_t (&bin)[4]) {
+    const uint4 k = *reinterpret_cast<const uint4*>(keys + min(i, (nc - 1) & ~3));
+    key[0] = k.x, key[1] = k.y, key[2] = k.z, key[3] = k.w;
 #pragma unroll
-  for (int w = 0; w < NW_SEL; ++w) top = max(top, (uint32_t)sm.wsum[w]);
-  for (int i = tid; i < nc; i += NT_SEL) {
-    const uint32_t bin = (top - keys[i]) >> 15;
-    if (bin < SEL_BINS) atomicAdd(&rk.bins[bin], 1);
+    for (int j = 0; j < 4; ++j) bin[j] = i + j < nc ? (top - key[j]) >> 15 : SEL_BINS;
+  };
+  uint32_t key[4], bin[4];
+  for (int i = 4 * tid; i < nc; i += 4 * NT_SEL) {
+    bins4(i, key, bin);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (bin[j] < SEL_BINS) atomicAdd(&rk.bins[bin[j]], 1);
   }
   __syncthreads();
   {
@@ -1014,7 +1023,6 @@ __device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, 
       const int o = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += o;
     }
-    __syncthreads();  // wsum held the maxima
     if (lane == 31) sm.wsum[wid] = incl;
     __syncthreads();
 #pragma unroll
@@ -1030,9 +1038,25 @@ __device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, 
   __syncthreads();
   const int last = sm.last;
   if (last >= 0) {
-    for (int i = tid; i < nc; i += NT_SEL) {
-      const uint32_t key = keys[i];
-      if ((top - key) >> 15 <= (uint32_t)last) rk.list[atomicAdd(&sm.count, 1)] = rank_entry(key, i);
+    for (int i0 = 0; i0 < nc; i0 += 4 * NT_SEL) {
+      const int i = i0 + 4 * tid;
+      bins4(i, key, bin);
+      uint32_t in[4];
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        in[j] = __ballot_sync(0xffffffffu, bin[j] <= (uint32_t)last);
+        n += __popc(in[j]);
+      }
+      if (n == 0) continue;
+      int at = lane == 0 ? atomicAdd(&sm.count, n) : 0;
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (bin[j] <= (uint32_t)last)
+          rk.list[at + __popc(in[j] & ((1u << lane) - 1u))] = rank_entry(key[j], i + j);
+        at += __popc(in[j]);
+      }
     }
     __syncthreads();
     sort_entries(rk, sm.count, kr);
@@ -1058,11 +1082,12 @@ __device__ void rank_keys(const uint32_t* keys, int nc, int kr, SelectSmem& sm, 
 // exchanged, they send the scores to the first, which ranks them.
 // Bound by its instructions and its chain of steps (page id, mean, products, two
 // exchanges, ranking), not by memory (0.6 TB/s, the 64-bit units a tenth busy): 8 KV
-// heads, d 128: 256 pages of one sequence 6.7 us, 4096 (of 16 tokens, 4 sequences)
-// 22.5 us, 1024 (16 sequences) 20.9 us.  Every CTA sorting its own pages and
+// heads, d 128: 256 pages of one sequence 6.8 us, 4096 (of 16 tokens, 4 sequences)
+// 22.2 us, 1024 (16 sequences) 20.4 us.  Every CTA sorting its own pages and
 // ranking them in the others' lists took 8.2, 25.7 and 22.4 us; CTAs of half as many threads
 // in clusters of 16, 38 us at 4 x 4096; the query in registers with the sums as
-// butterflies, 32 us; three CTAs to an SM, 30 us; one, 36 us.
+// butterflies, 32 us; an eighth of the dims and four pages a lane (half the reads of the
+// query, more exchanges), 24 us; three CTAs to an SM, 30 us; one, 36 us.
 // R: r rounded up to 4 or 8.
 template <int HD, typename T, int R>
 __global__ void __launch_bounds__(NT_SEL, 2)
@@ -1275,6 +1300,7 @@ __global__ void __launch_bounds__(NT_SEL, 2)
   __syncthreads();
   const uint32_t kbase = mapa_shared(smem_u32(keys), 0);
   bool odd = false;
+  uint32_t top = 0u;
   for (int i = tid; i < np; i += NT_SEL) {
     double sc = 0.0;
     for (int t = 0; t < p.r; ++t) sc += e[(size_t)t * p.ppc + i] * sm.f[t];
@@ -1283,13 +1309,16 @@ __global__ void __launch_bounds__(NT_SEL, 2)
       key = 0.f;
       odd = true;
     }
+    top = max(top, __float_as_uint(key));
     st_dsmem_u32(kbase + (uint32_t)(s0 + i) * 4u, __float_as_uint(key));
   }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) st_dsmem_u32(mapa_shared(smem_u32(&sm.top[rank][wid]), 0), top);
   if (odd) atomicOr(p.status, HYLRA_STATUS_NONFINITE);
   cluster_sync_all();
   if (rank != 0) return;
   RankSmem& rk = *reinterpret_cast<RankSmem*>(e);
-  rank_keys(keys, nc, kr, sm, rk);
+  rank_keys(keys, nc, kr, cs, sm, rk);
   for (int i = tid; i < kr; i += NT_SEL)
     dst[forced + i] = c0 + (int32_t)~(uint32_t)(rk.sorted[i] & 0xffffffffull);
 }
