@@ -1081,13 +1081,14 @@ __device__ void rank_keys(const uint32_t* keys, int nc, int kr, int cs, SelectSm
 // The CTAs of a cluster share the pages; once their maxima and sums have been
 // exchanged, they send the scores to the first, which ranks them.
 // Bound by its instructions and its chain of steps (page id, mean, products, two
-// exchanges, ranking), not by memory (0.6 TB/s, the 64-bit units a tenth busy): 8 KV
-// heads, d 128: 256 pages of one sequence 6.8 us, 4096 (of 16 tokens, 4 sequences)
-// 22.2 us, 1024 (16 sequences) 20.4 us.  Every CTA sorting its own pages and
-// ranking them in the others' lists took 8.2, 25.7 and 22.4 us; CTAs of half as many threads
-// in clusters of 16, 38 us at 4 x 4096; the query in registers with the sums as
-// butterflies, 32 us; an eighth of the dims and four pages a lane (half the reads of the
-// query, more exchanges), 24 us; three CTAs to an SM, 30 us; one, 36 us.
+// exchanges, ranking), not by memory (0.9 TB/s, the 64-bit units an eighth busy): 8 KV
+// heads, d 128: 256 pages of one sequence 6.8 us, 9362 of three (16 tokens each)
+// 22.2 us, 8423 of 16 20.4 us.  Every CTA sorting its own pages and ranking them in
+// the others' lists took 8.2, 25.7 and 22.4 us.  At 9362 pages, of that form: CTAs
+// of half as many threads in clusters of 16, 38 us; the query in registers with the
+// sums as butterflies, 32 us; three CTAs to an SM, 30 us; one, 36 us; and of this
+// one: an eighth of the dims and four pages a lane (half the reads of the query, more
+// exchanges), 24 us.
 // R: r rounded up to 4 or 8.
 template <int HD, typename T, int R>
 __global__ void __launch_bounds__(NT_SEL, 2)
@@ -1348,7 +1349,7 @@ struct AppendParams {
 // its page, the threads have summed the page's keys on the way.  Rows of the page
 // before the run come from the pool, or from the input where a token that was left out
 // parts two runs of this call.  Bound by memory: two rows read and two written a
-// token.  68 000 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
+// token.  63 132 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
 // copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
 // took 127-135 us, two rows in flight per thread do as well as four (eight: 118), and
 // 64 columns a CTA lose a fifth with 16-token pages.
@@ -1523,7 +1524,7 @@ __device__ __forceinline__ void scan2(long long& t, int& a, TablesSmem& sm) {
 // writes its share of slots and table entries; the last CTA to have read the
 // inputs writes the small outputs, which may be the inputs themselves.
 // Bound by latency: two scans, a search per token and the way of two dependent loads.
-// 16 requests of a token each 4.6 us, 1024 such 6.5 us, 68 000 new tokens of 64
+// 16 requests of a token each 4.6 us, 1024 such 6.5 us, 288 613 new tokens of 64
 // requests 8.6 us; a kernel for the sums before one for the slots would add a launch,
 // and the smallest one here (an append of 16 tokens) takes 1.9 us.
 __global__ void __launch_bounds__(NT_TAB)
