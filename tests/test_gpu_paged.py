@@ -506,6 +506,15 @@ def test_select_long(k):
     assert c.status() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,k", [(8, 1, 64, 1024), (4, 2, 128, 40)])
+def test_select_largest_table(hq, hkv, d, k):
+    """Every column of the longest table holds a page."""
+    c = T.make_cache((H.MAX_SEQLEN - 3, 50), 16, hq, hkv, d, "bf16", seed=k)
+    means = make_means(c, k)
+    assert np.array_equal(run_select(c, means, k, 2, 3), oracle_select(c, means, k, 2, 3))
+    assert c.status() == 0
+
+
 def test_select_many_heads():
     lens = tuple(int(x) for x in np.random.default_rng(3).integers(0, 2000, 150))
     c = T.make_cache(lens, 32, 8, 4, 64, "fp16", seed=3)
