@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(NTHR, 4)
     // for stages, so a copy could land in a stage still being read
     if (__any_sync(0xffffffffu, *abort_flag)) return;
     const int k = (i / NWC) & (UB - 1);
-    if (k == 0) fetch(i);
+    if (k == 0 && i >= NWC) fetch(i);
     // lanes 0..15 the boxes of K, 16..31 those of V: a box is 64 columns of a piece
     const int box = lane & 15, piece = box / S::HALVES, half = box % S::HALVES;
     const bool mine = piece < ppu;
@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(NTHR, 4)
                   lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
     }
   };
+  // every warp looks up its first pages now, and not when its turn comes: that would
+  // hold up the units' chain for a trip to memory (two with a list) per warp
+  fetch(cw);
   for (int i = 0; i < nst && i < n; ++i)  // nst <= 3: a different warp each
     if (i == cw) issue(i, i);
 
