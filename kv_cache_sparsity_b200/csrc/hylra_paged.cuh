@@ -153,8 +153,8 @@ struct DecodeParams {
 
 // A unit is UTOK tokens of one (sequence, KV head), read as pieces of
 // min(page size, UTOK) rows; warp w computes the logits of tokens 16*TT*w .. and,
-// for all of the unit's tokens, the dims 16*DT*w .. of O.  The warps request the
-// units in turn, each as soon as its stage is free.
+// for all of the unit's tokens, the dims 16*DT*w .. of O.  Each warp requests its
+// share of a unit's boxes as soon as the stage is free.
 template <int HD>
 struct DecodeShape {
   static constexpr int UTOK = STAGE_BYTES / (4 * HD);  // 64 (d = 128) or 128 (d = 64)
@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(NTHR, 4)
   }
   if (n == 0) return;
 
-  // Requests.  Unit i is warp i % 4's; a warp looks up the pages of its next
-  // 32 / (pieces of a unit) units at once, lane l those of piece l % ppu.
+  // Requests.  Every warp looks up the pages of 32 / (pieces of a unit) units at once,
+  // lane l those of piece l % ppu, and requests every fourth of a unit's boxes.
   const uint64_t pol = l2_evict_first_policy();
   const int ppu = 1 << ppl, UB = 32 >> ppl;
   int f_page = 0, f_row = 0, f_rows = 0, f_b = 0, f_h = 0, f_start = 0;
   auto fetch = [&](int base) {
     f_rows = f_start = 0;
-    const int ui = base + NWC * (lane >> ppl);
+    const int ui = base + (lane >> ppl);
     if (ui >= n) return;
     const Unit x = locate(up, p.B, p.Hkv, lo + ui);
     f_b = x.b;
@@ -384,25 +384,30 @@ __global__ void __launch_bounds__(NTHR, 4)
     f_row = first & (ps - 1);
     f_rows = max(0, min(1 << brl, len - (j << psl) - f_row));
   };
-  auto issue = [&](int i, int s) {  // unit i (this warp's) into stage s
-    // after a failed wait nothing more is requested: the others no longer wait
-    // for stages, so a copy could land in a stage still being read
-    if (__any_sync(0xffffffffu, *abort_flag)) return;
-    const int k = (i / NWC) & (UB - 1);
-    if (k == 0 && i >= NWC) fetch(i);
-    // lanes 0..15 the boxes of K, 16..31 those of V: a box is 64 columns of a piece
-    const int box = lane & 15, piece = box / S::HALVES, half = box % S::HALVES;
-    const bool mine = piece < ppu;
-    const int src = (k << ppl) + (mine ? piece : 0);
-    const int pg = __shfl_sync(0xffffffffu, f_page, src);
-    const int rw = __shfl_sync(0xffffffffu, f_rows, src);
-    const int r0 = __shfl_sync(0xffffffffu, f_row, src);
-    const int b = __shfl_sync(0xffffffffu, f_b, k << ppl);
-    const int h = __shfl_sync(0xffffffffu, f_h, k << ppl);
-    const int start = __shfl_sync(0xffffffffu, f_start, k << ppl);
-    const bool lead = lane < 16 && half == 0 && piece < MAX_PIECES;  // a lane per piece
-    const uint32_t np = __popc(__ballot_sync(0xffffffffu, lead && mine && rw > 0));
-    if (lead) sm.nv[s][piece] = mine ? rw : 0;
+  auto issue = [&](int i, int s) {  // this warp's share of unit i into stage s
+    const int k = i & (UB - 1), at = k << ppl;
+    if (k == 0) fetch(i);
+    // box: 64 columns of a piece of K or V; lanes 0..7 take every fourth
+    const int box = (lane & 7) * NWC + cw, piece = (box >> 1) / S::HALVES;
+    const int half = (box >> 1) % S::HALVES;
+    const bool mine = lane < 8 && piece < ppu, keys = (box & 1) == 0;
+    const int pg = __shfl_sync(0xffffffffu, f_page, at + (mine ? piece : 0));
+    const int rw = __shfl_sync(0xffffffffu, f_rows, at + (mine ? piece : 0));
+    const int r0 = __shfl_sync(0xffffffffu, f_row, at + (mine ? piece : 0));
+    const int h = __shfl_sync(0xffffffffu, f_h, at);
+    if (mine && rw > 0) {
+      uint8_t* dst = ring + s * STAGE_BYTES + (keys ? 0 : HALF) + half * S::HALF_BYTES +
+                     (piece << (brl + 7));
+      tma_load_5d(dst, keys ? &tmK : &tmV, 0, r0, half, h, pg, keys ? &sm.fullK[s] : &sm.fullV[s],
+                  pol);
+    }
+    if (cw != 0) return;
+    // warp 0 says what is to come; the bytes of a copy that is done before count too
+    const int rows = __shfl_sync(0xffffffffu, f_rows, at + (lane & (ppu - 1)));
+    const int b = __shfl_sync(0xffffffffu, f_b, at);
+    const int start = __shfl_sync(0xffffffffu, f_start, at);
+    const uint32_t np = __popc(__ballot_sync(0xffffffffu, lane < ppu && rows > 0));
+    if (lane < MAX_PIECES) sm.nv[s][lane] = lane < ppu ? rows : 0;
     __syncwarp();
     if (lane == 0) {
       const uint32_t qbytes = start ? (uint32_t)(p.r * HD * 2) : 0u;
@@ -417,18 +422,8 @@ __global__ void __launch_bounds__(NTHR, 4)
                   qbytes, &sm.fullK[s]);
     }
     __syncwarp();
-    if (mine && rw > 0) {
-      uint8_t* dst = ring + s * STAGE_BYTES + (lane < 16 ? 0 : HALF) + half * S::HALF_BYTES +
-                     (piece << (brl + 7));
-      tma_load_5d(dst, lane < 16 ? &tmK : &tmV, 0, r0, half, h, pg,
-                  lane < 16 ? &sm.fullK[s] : &sm.fullV[s], pol);
-    }
   };
-  // every warp looks up its first pages now, and not when its turn comes: that would
-  // hold up the units' chain for a trip to memory (two with a list) per warp
-  fetch(cw);
-  for (int i = 0; i < nst && i < n; ++i)  // nst <= 3: a different warp each
-    if (i == cw) issue(i, i);
+  for (int i = 0; i < nst && i < n; ++i) issue(i, i);
 
   const int g4 = lane >> 2, c4 = lane & 3, mi = lane >> 3, xr = lane & 7;
   const int h0 = 2 * c4, h1 = 2 * c4 + 1;  // this lane's heads in the C fragments
@@ -453,6 +448,7 @@ __global__ void __launch_bounds__(NTHR, 4)
   float m_run[2], z_run[2];
   Unit x = locate(up, p.B, p.Hkv, lo);
   bool has_start = false;  // this CTA holds the segment's first unit
+  int stop = 0;            // a wait has failed
   int s = 0;
   uint32_t ph = 0;
 
@@ -581,7 +577,10 @@ __global__ void __launch_bounds__(NTHR, 4)
       }
       fence_proxy_async_smem();
     }
-    __syncthreads();  // P and the zeroed rows of all warps
+    // P and the zeroed rows of all warps.  After a failed wait nothing more is
+    // requested: the others no longer wait for stages, so a copy could land in a stage
+    // still being read.  All warps must agree on it, or a copy would not be waited for.
+    stop |= __syncthreads_or(*abort_flag);
     // O^T += V^T P^T; the matrix unit's sums cover this unit, the running ones are fp32
     float acc[E::SPLIT][DT][4];
 #pragma unroll
@@ -609,12 +608,12 @@ __global__ void __launch_bounds__(NTHR, 4)
           for (int u = 0; u < E::SPLIT; ++u) E::mma(acc[u][t], vf, pf[u][2 * c], pf[u][2 * c + 1]);
         }
     }
-    // the stage is free once all warps are here; the warp whose turn it is
-    // requests the next unit before it waits for the data of another
+    // the stage is free once all warps are here
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
-    if (i + nst < n && ((i + nst) & (NWC - 1)) == cw) {
+    if (i + nst < n && !stop) {
       mbar_wait_bounded(&sm.empty[s], ph, abort_flag, p.wait_limit);
+      __syncwarp();
       issue(i + nst, s);
     }
 #pragma unroll
