@@ -282,13 +282,15 @@ __device__ __forceinline__ void sum_units(const DecodeParams& p, int* up) {
 // heads) would be as empty and need its accumulators moved to registers for the
 // softmax, so the warps' own matrix instructions are used (16 % of their rate).
 // Bound by memory: each key and value is read once.  16 sequences of up to 128K, 8 KV
-// heads, d 128: 616 us back to back, 6.8 TB/s; one of 32K: 29 us, of which about 3 are
+// heads, d 128: 618 us back to back, 6.8 TB/s; one of 32K: 29 us, of which about 3 are
 // the way to the first data and 5 the last CTAs and the join; in between 6.1 TB/s.
 // Three CTAs of four warps and two 32 KB stages to an SM: one CTA of nine warps with
 // three 64 KB stages waited for its own arithmetic (697 us; a unit's chain of steps
 // takes 1 us whatever its size), two CTAs with three stages each take 650 us.  A
 // common maximum first, one barrier more than weights relative to each warp's own,
-// costs nothing and saves a rescaling path.
+// costs nothing and saves a rescaling path.  One warp in turn requesting a whole unit
+// held up the others: 142 instead of 135 us over 4 sequences of 64K..128K in pages of 16
+// (d 64), 29.3 instead of 28.9 us over one of 32K.
 template <int HD, typename T, bool LIST>
 __global__ void __launch_bounds__(NTHR, 4)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
