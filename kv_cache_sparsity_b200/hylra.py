@@ -10,6 +10,7 @@ shared library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -406,7 +407,6 @@ class _Forms:
 
     def __init__(self, s: PagedShape):
         import torch
-        self.key = bytes(s)
         self.torch = torch
         self.dtype = torch.bfloat16 if s.dtype == BF16 else torch.float16
         self.pool = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)
@@ -417,14 +417,16 @@ class _Forms:
         self.lse = (s.batch, s.num_q_heads)
         self.heads = (s.batch, s.num_kv_heads)
         self.means = (s.num_pages, s.num_kv_heads, s.head_dim)
-        self.ref = ctypes.byref(s)
+
+
+@functools.lru_cache(maxsize=256)
+def _forms_of(fields: bytes) -> _Forms:
+    return _Forms(PagedShape.from_buffer_copy(fields))
 
 
 def _forms(s: PagedShape) -> _Forms:
-    f = s.__dict__.get("_forms")
-    if f is None or f.key != bytes(s):  # made again when a field has changed
-        f = s.__dict__["_forms"] = _Forms(s)
-    return f
+    # by the fields' values: the shape may be changed, copied and pickled between calls
+    return _forms_of(bytes(s))
 
 
 def _want_pools(f: _Forms, K, V, dev):
@@ -503,7 +505,7 @@ def paged_tables(shape: PagedShape, cached_lens, new_lens, free_pages, free_coun
                            ("slot_map", slot_map, (nslots,)),
                            ("free_count_out", free_count_out, (1,))):
             _want(what, t, i32, n, dev)
-    _paged_call(f.torch, (_lib or load()).hylra_paged_tables, ws, dev, stream, f.ref,
+    _paged_call(f.torch, (_lib or load()).hylra_paged_tables, ws, dev, stream, ctypes.byref(shape),
                 cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), nfree,
                 free_count.data_ptr(), block_table.data_ptr(), seqlens_out.data_ptr(),
                 cu_new.data_ptr(), slot_map.data_ptr(), nslots, free_count_out.data_ptr())
@@ -533,7 +535,7 @@ def paged_append(shape: PagedShape, K_new, V_new, slot_map, K_pages, V_pages, ke
                                       and key_means.is_contiguous()
                                       and key_means.get_device() == dev):
         _want("key_means", key_means, t, f.means, dev)
-    _paged_call(f.torch, (_lib or load()).hylra_paged_append, ws, dev, stream, f.ref,
+    _paged_call(f.torch, (_lib or load()).hylra_paged_append, ws, dev, stream, ctypes.byref(shape),
                 K_new.data_ptr(), V_new.data_ptr(), ks[0] if n > 1 else H * d,
                 slot_map.data_ptr(), n, K_pages.data_ptr(), V_pages.data_ptr(),
                 None if key_means is None else key_means.data_ptr())
@@ -546,7 +548,7 @@ def paged_decode(shape: PagedShape, q, K_pages, V_pages, block_table, seqlens, o
     _want_query(f, q, block_table, seqlens, dev)
     _want_pools(f, K_pages, V_pages, dev)
     _want_result(f, out, lse, dev)
-    _paged_call(f.torch, (_lib or load()).hylra_paged_decode, ws, dev, stream, f.ref,
+    _paged_call(f.torch, (_lib or load()).hylra_paged_decode, ws, dev, stream, ctypes.byref(shape),
                 q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
                 seqlens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr())
 
@@ -568,7 +570,7 @@ def paged_select(shape: PagedShape, q, key_means, block_table, seqlens, page_idx
             and key_means.is_contiguous() and key_means.get_device() == dev):
         _want("key_means", key_means, f.dtype, f.means, dev)
     k = _want_list(f, page_idx, dev)
-    _paged_call(f.torch, (_lib or load()).hylra_paged_select, ws, dev, stream, f.ref,
+    _paged_call(f.torch, (_lib or load()).hylra_paged_select, ws, dev, stream, ctypes.byref(shape),
                 q.data_ptr(), key_means.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
                 k, sink, recent, page_idx.data_ptr())
 
@@ -581,7 +583,7 @@ def paged_decode_topk(shape: PagedShape, q, K_pages, V_pages, block_table, seqle
     _want_pools(f, K_pages, V_pages, dev)
     k = _want_list(f, page_idx, dev)
     _want_result(f, out, lse, dev)
-    _paged_call(f.torch, (_lib or load()).hylra_paged_decode_topk, ws, dev, stream, f.ref,
+    _paged_call(f.torch, (_lib or load()).hylra_paged_decode_topk, ws, dev, stream, ctypes.byref(shape),
                 q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
                 seqlens.data_ptr(), page_idx.data_ptr(), k, out.data_ptr(),
                 None if lse is None else lse.data_ptr())

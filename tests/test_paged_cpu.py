@@ -1,8 +1,10 @@
 """Paged-cache calls without a GPU: refusals before any launch, the binding's
 checks, and pins of the 64-bit oracle."""
 
+import copy
 import ctypes
 import math
+import pickle
 
 import numpy as np
 import pytest
@@ -154,6 +156,68 @@ def test_binding_checks_tensors(lib):
             args[at] = v
             with pytest.raises(ValueError):
                 H.paged_decode(*args)
+
+
+class _FakeCuda:
+    """A tensor's description without its memory: what the binding looks at."""
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev = t, dev
+        self.dtype, self.shape, self.nbytes = t.dtype, t.shape, t.nbytes
+        self.device = f"cuda:{dev}"
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The paged calls reach a recorder in the library's place: (name, shape's fields, stream)."""
+    made = []
+
+    def entry(name):
+        def call(shape, *args):
+            made.append((name, bytes(shape._obj), args[-1]))
+            return 0
+        call.__name__ = name
+        return call
+
+    class Recorder:
+        def __getattr__(self, name):
+            return entry(name)
+
+    monkeypatch.setattr(H, "_lib", Recorder())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    return made
+
+
+def _decode_args(shape):
+    s, t = shape, torch.bfloat16
+    pool = torch.empty(s.num_pages, s.num_kv_heads, s.page_size, s.head_dim, dtype=t)
+    return [shape] + [_FakeCuda(x) for x in (
+        torch.empty(s.batch, s.num_q_heads, s.head_dim, dtype=t), pool, pool,
+        torch.empty(s.batch, s.max_pages, dtype=torch.int32), torch.empty(s.batch, dtype=torch.int32),
+        torch.empty(s.batch, s.num_q_heads, s.head_dim), torch.empty(4096, dtype=torch.uint8))]
+
+
+def test_shapes_changed_and_copied_between_calls(calls):
+    """The library gets the fields that the tensors were checked against."""
+    a = _shape()
+    H.paged_decode(*_decode_args(a))
+    for copied in (copy.copy(a), copy.deepcopy(a), pickle.loads(pickle.dumps(a))):
+        before = _decode_args(copied)
+        a.batch += 1  # the copy keeps its own fields
+        H.paged_decode(*before)
+        assert calls[-1][1] == bytes(copied) and copied.batch == 2
+        with pytest.raises(ValueError):
+            H.paged_decode(a, *before[1:])
+        H.paged_decode(*_decode_args(a))
+        assert calls[-1][1] == bytes(a)
+        a.batch = 2
 
 
 # ------------------------------------------------------------ oracle pins
