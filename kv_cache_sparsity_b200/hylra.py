@@ -9,6 +9,7 @@ shared library is missing or a call fails, an exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -177,9 +178,20 @@ def workspace_bytes(shape: Shape) -> int:
     return n.value
 
 
+def _on_device_of(ws):
+    """Context in which the workspace's device is the current one."""
+    import torch
+    dev = ws.get_device()
+    if dev < 0 or dev == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
 def workspace_init(ws, stream=None):
-    _check(load().hylra_workspace_init(_ptr(ws), ws.numel() * ws.element_size(),
-                                       _stream(stream)), "hylra_workspace_init")
+    """Zero a workspace, on its device's current stream unless given another."""
+    with _on_device_of(ws):
+        _check(load().hylra_workspace_init(_ptr(ws), ws.numel() * ws.element_size(),
+                                           _stream(stream)), "hylra_workspace_init")
 
 
 def decode_full(shape: Shape, q, K, V, seqlens, out, topk_out, ws, stream=None):
@@ -240,9 +252,11 @@ def set_wait_limit(cycles: int):
 
 
 def read_status(ws, clear: bool = True, stream=None) -> int:
+    """The workspace's status word, read on its device's current stream unless given another."""
     v = ctypes.c_uint32(0)
-    _check(load().hylra_read_status(_ptr(ws), ctypes.byref(v), int(clear), _stream(stream)),
-           "hylra_read_status")
+    with _on_device_of(ws):
+        _check(load().hylra_read_status(_ptr(ws), ctypes.byref(v), int(clear), _stream(stream)),
+               "hylra_read_status")
     return v.value
 
 

@@ -220,6 +220,46 @@ def test_shapes_changed_and_copied_between_calls(calls):
         a.batch = 2
 
 
+def test_workspace_calls_run_on_the_workspaces_device(calls, monkeypatch):
+    """A workspace of another device than the current one is zeroed and read on the stream that the
+    paged calls with it use."""
+    current = [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Stream:
+        cuda_stream = property(lambda self: 100 + current[0])
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    made = []
+    lib = H._lib
+    for name in ("hylra_workspace_init", "hylra_read_status"):
+        monkeypatch.setattr(type(lib), name, staticmethod(
+            lambda *args, name=name: made.append((name, current[0], args[-1])) or 0), raising=False)
+    for dev in (0, 1):
+        args = _decode_args(_shape())
+        for t in args[1:]:
+            t.dev = dev
+        H.workspace_init(args[-1])
+        H.paged_decode(*args)
+        H.read_status(args[-1])
+        assert calls[-1][2] == 100 + dev
+        assert made[-2:] == [("hylra_workspace_init", dev, 100 + dev),
+                             ("hylra_read_status", dev, 100 + dev)]
+        assert current[0] == 0
+
+
 # ------------------------------------------------------------ oracle pins
 
 
