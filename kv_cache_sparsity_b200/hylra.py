@@ -421,6 +421,8 @@ class _Forms:
 
     def __init__(self, s: PagedShape):
         import torch
+        if s.dtype not in (BF16, FP16):  # as the library answers for such a shape
+            raise HylraError(-2 if s.dtype == FP32 else -1, f"PagedShape.dtype {s.dtype}")
         self.torch = torch
         self.dtype = torch.bfloat16 if s.dtype == BF16 else torch.float16
         self.pool = (s.num_pages, s.num_kv_heads, s.page_size, s.head_dim)

@@ -260,6 +260,18 @@ def test_workspace_calls_run_on_the_workspaces_device(calls, monkeypatch):
         assert current[0] == 0
 
 
+@pytest.mark.parametrize("dtype,code", [(H.FP32, UNSUPPORTED), (7, INVALID)])
+def test_type_of_a_shape_refused_by_name(calls, dtype, code):
+    """A type that the paged calls lack is what is refused, not a tensor that has it."""
+    args = _decode_args(_shape())
+    args[0].dtype = dtype
+    for t in args[1:4]:
+        t.dtype = torch.float32
+    with pytest.raises(H.HylraError) as e:
+        H.paged_decode(*args)
+    assert e.value.code == code and not calls
+
+
 # ------------------------------------------------------------ oracle pins
 
 
