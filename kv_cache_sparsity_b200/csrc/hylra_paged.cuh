@@ -1151,13 +1151,15 @@ __global__ void __launch_bounds__(NT_SEL, 2)
   auto page_at = [&](int at) {
     return at < np ? __ldcg(p.table + (size_t)b * p.max_pages + c0 + s0 + at) : -1;
   };
+  // an entry outside the pool stands for no mean: zeros, so that what any page's
+  // mean holds stays out of the test for infinity and NaN below
   auto load_mean = [&](int at, int pg, uint4 (&u)[NV]) {
     const bool ok = pg >= 0 && pg < p.num_pages;
     if (!ok && at < np) atomicOr(p.status, HYLRA_STATUS_BAD_INDEX);
     const uint4* src = reinterpret_cast<const uint4*>(
         static_cast<const T*>(p.means) + ((size_t)(ok ? pg : 0) * p.Hkv + h) * HD + c * 8);
 #pragma unroll
-    for (int t = 0; t < NV; ++t) u[t] = at < np ? __ldcg(src + 4 * t) : make_uint4(0u, 0u, 0u, 0u);
+    for (int t = 0; t < NV; ++t) u[t] = ok ? __ldcg(src + 4 * t) : make_uint4(0u, 0u, 0u, 0u);
     return ok;
   };
   uint4 u[2][NV];

@@ -319,7 +319,6 @@ def test_decode_sharp_and_scaled():
     c.keys[p, 0, 5] = 4 * c.q[0, 1]
     T.check_attention(c, c.decode(), oracle_decode(c))
 
-
 def test_decode_non_finite_inputs_stay_in_their_rows():
     c = T.make_cache((700, 300), 32, 4, 2, 128, "bf16", seed=2)
     want = oracle_decode(c)
@@ -583,6 +582,33 @@ def test_select_bad_input():
     c.table[0, best] = -1
     got = run_select(c, means, 38, 1, 1)
     assert best not in got[0, 0].tolist()
+    assert c.status() == H.STATUS_BAD_INDEX
+
+
+@pytest.mark.parametrize("fill", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(4, 2, 64, "bf16"), (8, 1, 128, "fp16")])
+def test_select_bad_entries_beside_a_page_without_a_mean(fill, hq, hkv, d, dtype):
+    """A table entry outside the pool scores 0 and changes no other score, whatever the means of
+    pages that no sequence holds are."""
+    n = 700
+    c = T.make_cache((16 * n, 100), 16, hq, hkv, d, dtype, seed=15)
+    means = make_means(c)
+    held = torch.cat([c.table[0], c.table[1, :7]]).long()
+    if (held == 0).any():  # page 0 is no sequence's: another takes its place
+        spare = sorted(set(range(c.keys.shape[0])) - set(held.tolist()))[0]
+        means[spare] = means[0]
+        c.table[c.table == 0] = spare
+    means[0] = fill
+    bad = {7: -1, 8: 2**30, 300: c.keys.shape[0], 650: -(2**31)}
+    # the others rank as in a sequence without these pages
+    keep = [j for j in range(n) if j not in bad]
+    want = O.select(T.f64(c.q)[:1], T.f64(means), c.table.cpu().numpy()[:1, keep], (16 * len(keep),),
+                    16, c.scale, len(keep), 1, 1)[0][0]
+    for j, page in bad.items():
+        c.table[0, j] = page
+    got = run_select(c, means, n, 1, 1)[0]
+    assert np.array_equal(got[:, : len(keep)], np.array(keep)[want])
+    assert np.array_equal(got[:, len(keep):], [sorted(bad)] * hkv)
     assert c.status() == H.STATUS_BAD_INDEX
 
 
