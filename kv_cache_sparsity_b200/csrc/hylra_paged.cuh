@@ -75,9 +75,10 @@ struct Elem;
 // value would cost 2^-9 (bf16) of every weight in a result that is kept in
 // fp32, so P goes in as a sum of 16-bit terms: three bf16 terms hold all 24
 // bits of an fp32 value, two fp16 terms 22 bits.  fp16 has few exponents: P is
-// scaled by 2^12 there (P <= 1, so the first term stays below 65504), which
-// keeps the second term's rounding below 2^-36 of the largest weight.  The
-// scale cancels in O / Z.
+// scaled by 2^12 there.  P <= 1, logits being subtracted from their maximum before
+// they are scaled, so the first term stays below 65504; two terms are off by 2^-22
+// of a weight at most, or by 2^-37 of the largest possible one where the second is
+// subnormal.  The scale cancels in O / Z.
 template <>
 struct Elem<__nv_bfloat16> {
   static constexpr int SPLIT = 3;
@@ -163,7 +164,7 @@ struct DecodeShape {
   static constexpr int DT = HD / (16 * NWC);
   static constexpr int HALVES = HD / 64;        // 64-column boxes of a row
   static constexpr int HALF_BYTES = UTOK * 128; // one half of all rows: [token][128 bytes]
-  static constexpr int SLOT = GRP * HD + 2 * GRP;  // partial: O, m, Z
+  static constexpr int SLOT = GRP * HD + 2 * GRP;  // partial: O, m (a raw logit), Z
 };
 
 template <int HD, int SPLIT>
@@ -525,17 +526,18 @@ __global__ void __launch_bounds__(NTHR, 4)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float4 u = *reinterpret_cast<const float4*>(sm.mx[e ? h1 : h0]);
-      m_new[e] = fmaxf(m_run[e], fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)) * sl);
+      m_new[e] = fmaxf(m_run[e], fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)));
       sub[e] = m_new[e] == -INFINITY ? 0.f : m_new[e];  // nothing attended to yet: weights 0
     }
     // weights relative to the running maximum, split into 16-bit terms: both heads
-    // of a token in one word
+    // of a token in one word.  Maxima are raw logits: a product with the scale minus
+    // a rounded one may be above 0, by 2^-24 of a logit, which at 2^27 is 8 binades
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        float w0 = ex2_approx(fmaf(a[t][e], sl, -sub[0])) * E::SCALE;
-        float w1 = ex2_approx(fmaf(a[t][e + 1], sl, -sub[1])) * E::SCALE;
+        float w0 = ex2_approx((a[t][e] - sub[0]) * sl) * E::SCALE;
+        float w1 = ex2_approx((a[t][e + 1] - sub[1]) * sl) * E::SCALE;
         sum[0] += w0;
         sum[1] += w1;
 #pragma unroll
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(NTHR, 4)
     if (m_new[0] != m_run[0] || m_new[1] != m_run[1]) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float al = ex2_approx(m_run[e] - sub[e]);
+        const float al = ex2_approx((m_run[e] - sub[e]) * sl);
         z_run[e] *= al;
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(NTHR, 4)
         if (whole) {
           if (p.lse && stats)
             p.lse[row] = z == 0.f ? -INFINITY
-                                  : (m_run[e] + (log2f(z) - E::SHIFT)) * 0.69314718f;
+                                  : fmaf(m_run[e], sl, log2f(z) - E::SHIFT) * 0.69314718f;
         } else {
           float* slot = p.partials + (size_t)(2 * (int)blockIdx.x + (has_start ? 1 : 0)) * S::SLOT;
           if (stats) {
@@ -740,6 +742,7 @@ __global__ void __launch_bounds__(NT_JOIN)
   }
   griddep_wait();
   if (nc < 2) return;
+  const float sl = p.scale_log2;
   const int ncol = r * (HD / 4);
   for (int col0 = (int)blockIdx.y * 32; col0 < ncol; col0 += (int)gridDim.y * 32) {
     const int col = min(col0 + lane, ncol - 1), g = col / (HD / 4);
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(NT_JOIN)
 #pragma unroll
       for (int u = 0; u < CB; ++u) mn = fmaxf(mn, mc[u]);
       const float ms = mn == -INFINITY ? 0.f : mn;
-      const float al = ex2_approx(m - ms);
+      const float al = ex2_approx((m - ms) * sl);
       acc.x *= al;
       acc.y *= al;
       acc.z *= al;
@@ -771,7 +774,7 @@ __global__ void __launch_bounds__(NT_JOIN)
 #pragma unroll
       for (int u = 0; u < CB; ++u) {
         if (c0 + u * NG >= nc) break;
-        const float f = ex2_approx(mc[u] - ms);
+        const float f = ex2_approx((mc[u] - ms) * sl);
         z = fmaf(f, zc[u], z);
         acc.x = fmaf(f, o[u].x, acc.x);
         acc.y = fmaf(f, o[u].y, acc.y);
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(NT_JOIN)
       float zz = 0.f;
 #pragma unroll
       for (int w = 0; w < NG; ++w) {
-        const float f = ex2_approx(wm[w][lane] - ms);
+        const float f = ex2_approx((wm[w][lane] - ms) * sl);
         const float4 x = wacc[w][lane];
         zz = fmaf(f, wz[w][lane], zz);
         v.x = fmaf(f, x.x, v.x);
@@ -806,7 +809,8 @@ __global__ void __launch_bounds__(NT_JOIN)
       *reinterpret_cast<float4*>(p.out + row * HD + 4 * (col % (HD / 4))) =
           make_float4(v.x * rz, v.y * rz, v.z * rz, v.w * rz);
       if (p.lse && col % (HD / 4) == 0)
-        p.lse[row] = zz == 0.f ? -INFINITY : (mn + (log2f(zz) - Elem<T>::SHIFT)) * 0.69314718f;
+        p.lse[row] = zz == 0.f ? -INFINITY
+                               : fmaf(mn, sl, log2f(zz) - Elem<T>::SHIFT) * 0.69314718f;
     }
     __syncthreads();
   }

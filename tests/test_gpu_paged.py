@@ -319,6 +319,33 @@ def test_decode_sharp_and_scaled():
     c.keys[p, 0, 5] = 4 * c.q[0, 1]
     T.check_attention(c, c.decode(), oracle_decode(c))
 
+@pytest.mark.parametrize("dtype,d,size", [("fp16", 64, 60000.0), ("fp16", 128, 60000.0),
+                                          ("bf16", 128, 1e15), ("bf16", 64, -3e9)])
+@pytest.mark.parametrize("n", [70, 9000])
+def test_decode_very_large_logits(dtype, d, size, n):
+    """Logits of up to 2^100: the largest keys' weights are 1, the others 0.
+
+    Queries and keys lie along the first dimension, so that a raw logit is one exact product and
+    equal keys give equal logits.  The other keys are half as long or zero: their logits are 2^27 or
+    more below, weights of 0 in 64 bits too.  out: a sum of values below 6, with 2^-23 of the sum of
+    their magnitudes for an addition: 128 of them in a tile, one for each of at most n / 64 tiles and
+    256 CTAs, and a division.  lse: the scale, its product with the logit, the sum with the logarithm
+    and the change of its base round once each, and the base's constant is rounded: 5 * 2^-24."""
+    c = T.make_cache((n, 33), 64, 4, 1, d, dtype, seed=n)
+    c.keys.zero_()
+    c.q.zero_()
+    c.q[:, :, 0] = size
+    for b, length in enumerate(c.lens):
+        for i in range(length):
+            c.keys[int(c.table[b, i // 64]), 0, i % 64, 0] = (1, 0.5, 0)[i % 3] * size
+    want, l_ref = oracle_decode(c)
+    every = torch.arange(c.shape.max_pages, dtype=torch.int32, device="cuda").expand(2, 1, -1)
+    for out, lse in (c.decode(), c.decode_topk(every.contiguous())):
+        assert np.abs(T.f64(out) - want).max() <= 6 * (128 + n / 64 + 256 + 2) * 2.0**-23
+        assert np.all(np.abs(T.f64(lse) - l_ref) <= 5 * 2.0**-24 * np.abs(l_ref))
+    assert c.status() == 0
+
+
 def test_decode_non_finite_inputs_stay_in_their_rows():
     c = T.make_cache((700, 300), 32, 4, 2, 128, "bf16", seed=2)
     want = oracle_decode(c)
