@@ -365,7 +365,8 @@ typedef struct hylra_paged {
   int64_t page_stride;  /* strides in elements: multiples of 8, below 2^39;            */
   int64_t head_stride;  /*   rows of d elements must not overlap (the stride of a      */
   int64_t token_stride; /*   dimension of extent 1 is not used)                        */
-  float softmax_scale;  /* logit scale; 0: 1/sqrt(d).  Finite, >= 0                    */
+  float softmax_scale;  /* logit scale; 0: 1/sqrt(d).  Finite, >= 0; <= 2^126 in the
+                           decode calls                                                */
 } hylra_paged_t;
 
 /* Bytes of workspace the paged calls need on the current device.  One size

@@ -217,6 +217,8 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
     return HYLRA_ERR_INVALID;
   if (use_list && (bad_ptr(list, 4) || k < 1)) return HYLRA_ERR_INVALID;
   if (use_list && k > HYLRA_MAX_TOPK) return HYLRA_ERR_UNSUPPORTED;
+  // the scale times log2(e) must be an fp32 number
+  if (s->softmax_scale > 0x1p126f) return HYLRA_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if ((rc = current_device(&dev, &sms))) return rc;
   const PagedLayout L = make_layout(sms);

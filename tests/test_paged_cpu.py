@@ -116,6 +116,15 @@ def test_arguments_refused(lib, kw, code, who):
             assert rc == code, name
 
 
+def test_scale_past_fp32_refused(lib):
+    """A scale whose product with log2(e) no fp32 number holds; the selection works in 64 bits."""
+    big = dict(_calls(lib, _shape(scale=2.0**127)))
+    ok = dict(_calls(lib, _shape(scale=2.0**126)))
+    for name in ("decode", "topk"):
+        assert big[name] == UNSUPPORTED and ok[name] != UNSUPPORTED
+    assert big["select"] != UNSUPPORTED
+
+
 def test_null_shape(lib):
     assert all(rc == INVALID for _, rc in _calls(lib, None))
     assert lib.hylra_paged_workspace_bytes(None, None) == INVALID
