@@ -38,8 +38,11 @@ PTR = 1 << 20
 
 
 def _calls(lib, shape, **kw):
-    """Return codes of every entry point for this shape, with the given arguments changed."""
-    a = dict(q=PTR, K=PTR, V=PTR, table=PTR, lens=PTR, out=PTR, lse=None, ws=PTR, nbytes=1 << 30,
+    """Return codes of every entry point for this shape, with the given arguments changed.
+
+    The workspace is too small for any call: one whose arguments all pass ends there, the last check
+    before a launch, and no launch with these addresses happens on a machine with a GPU."""
+    a = dict(q=PTR, K=PTR, V=PTR, table=PTR, lens=PTR, out=PTR, lse=None, ws=PTR, nbytes=1,
              k=4, idx=PTR, means=PTR, sink=1, recent=1, new_stride=256, tokens=3, slots=PTR,
              free_cap=5, slot_cap=5)
     a.update(kw)
@@ -128,6 +131,15 @@ def test_scale_past_fp32_refused(lib):
 def test_null_shape(lib):
     assert all(rc == INVALID for _, rc in _calls(lib, None))
     assert lib.hylra_paged_workspace_bytes(None, None) == INVALID
+
+
+# what a call with good arguments ends with: the device query or, past it, the workspace check
+PASSED = {-3, -4}
+
+
+def test_calls_of_these_tests_end_before_a_launch(lib):
+    assert {rc for _, rc in _calls(lib, _shape())} <= PASSED
+    assert dict(_calls(lib, _shape(), tokens=0))["append"] in PASSED
 
 
 @pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3)])
