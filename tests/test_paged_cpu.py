@@ -154,6 +154,25 @@ def test_layouts_accepted(lib, order):
     assert all(codes[n] != UNSUPPORTED for n in POOL)
 
 
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3), (1, 0, 2, 3),
+                                   (1, 2, 0, 3), (2, 1, 0, 3)])
+def test_layouts_pass_the_pool_check(lib, order):
+    """Every order of the dimensions, padded rows and slices, down to the workspace check; the same
+    with one stride eight elements less than its rows and their padding allow is refused."""
+    extents = (10, 2, 16, 128)
+    for row in (128, 136, 256):
+        t = torch.empty([extents[i] for i in order[:3]] + [row], dtype=torch.bfloat16)[..., :128]
+        t = t.permute([order.index(i) for i in range(4)])
+        codes = dict(_calls(lib, _shape(pool=t)))
+        assert {codes[n] for n in POOL} <= PASSED
+        for at, name in enumerate(("page_stride", "head_stride", "token_stride")):
+            # what stands before the next element of the dimension ends in one row's padding
+            codes = dict(_calls(lib, _shape(pool=t, **{name: t.stride(at) - (row - 128) - 8})))
+            assert {codes[n] for n in POOL} == {INVALID}
+            codes = dict(_calls(lib, _shape(pool=t, **{name: t.stride(at) - (row - 128)})))
+            assert {codes[n] for n in POOL} <= PASSED
+
+
 def test_binding_checks_tensors(lib):
     s = _shape()
     pool = torch.zeros(10, 2, 16, 128, dtype=torch.bfloat16)
