@@ -411,8 +411,9 @@ int hylra_paged_tables(const hylra_paged_t* shape, const int32_t* cached_lens,
  * >= Hkv * d, so a slice of a fused projection's rows will do; num_tokens may
  * be 0).  slot_map: int32 [num_tokens]; -1 leaves a token out, any other value
  * outside the pool does so with HYLRA_STATUS_BAD_INDEX.  A sequence's tokens
- * must be in order and next to each other, and no slot may be named twice
- * (hylra_paged_tables gives such maps).
+ * must be in order, with no other sequence's between them, and no slot may be
+ * named twice (hylra_paged_tables gives such maps); tokens that are left out may
+ * stand anywhere.
  * key_means ([num_pages][Hkv][d], may be NULL): a token that lands in the last
  * row of its page makes the page full, and its mean key over all page_size
  * rows (earlier rows from this call or from the pool) is written there: summed

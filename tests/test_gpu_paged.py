@@ -223,6 +223,48 @@ def test_append_skips_slots():
     assert check_append(case, 16, slots) == H.STATUS_BAD_INDEX
 
 
+def with_left_out(case, gaps):
+    """The case with gaps[i] tokens that are left out before its token i, which take no slot."""
+    shape, keys, vals, means, k_new, v_new, slots = case
+    at = np.concatenate([[-1] * gaps.get(i, 0) + [i] for i in range(len(slots) + 1)])[:-1]
+    rows = torch.from_numpy(np.maximum(at, 0)).cuda()
+    out = torch.from_numpy(at < 0).cuda()[:, None, None]
+    nan = torch.full_like(k_new[:1], math.nan)
+    return (shape, keys, vals, means, torch.where(out, nan, k_new[rows]),
+            torch.where(out, nan, v_new[rows]), [slots[i] if i >= 0 else -1 for i in at])
+
+
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("gap", [1, 2, 50, 256, 1000])
+def test_append_left_out_tokens_inside_a_page(page, gap):
+    """Tokens left out between two of a page's: its mean takes the rows before them from this call."""
+    held, new = [0, 5, page - 2, 3, 0, page // 2], [page, page, 2, 3 * page + 7, 2 * page, 2]
+    case = append_case(held, new, page, d=64, dtype="fp16", layout="nhd", seed=gap)
+    first = np.cumsum([0] + new)
+    places = [5, page - 1, page + 3, 2 * page + 1, first[3] + page, first[3] + page + 4, first[5] + 1]
+    case = with_left_out(case, {int(i): gap for i in places})
+    assert check_append(case, page) == 0
+
+
+@pytest.mark.parametrize("tokens,page,hkv", [(500, 16, 2), (3000, 64, 1), (40000, 128, 1),
+                                             (40000, 16, 3)])
+def test_append_left_out_tokens_anywhere(tokens, page, hkv):
+    """Tiles of every size, gaps inside them, at their edges and over several."""
+    rng = np.random.default_rng(tokens + page)
+    lens = [tokens // 3, 1, tokens // 3, tokens - 1 - 2 * (tokens // 3)]
+    case = append_case([3, page - 1, 0, 1], lens, page, hkv=hkv, d=64, seed=tokens)
+    places = rng.choice(tokens + 1, tokens // 6, replace=False)
+    gaps = {int(i): int(g) for i, g in zip(places, rng.choice([1, 1, 2, 3, 70], len(places)))}
+    assert check_append(with_left_out(case, gaps), page) == 0
+
+
+def test_append_bad_slots_inside_a_page():
+    """A slot outside the pool leaves its token out, as -1 does, and says so."""
+    case = with_left_out(append_case([0, 2], [40, 30], 16, seed=1), {7: 1, 20: 3, 50: 2})
+    slots = [s if s >= 0 else (-7, 2**30)[i % 2] for i, s in enumerate(case[6])]
+    assert check_append(case, 16, slots) == H.STATUS_BAD_INDEX
+
+
 def test_append_without_means_and_without_tokens():
     shape, keys, vals, means, k_new, v_new, slots = append_case([0], [33], 16)
     ws = T.workspace(shape)
