@@ -55,7 +55,9 @@
  *    slots k'..k-1 hold -1.
  *  * One workspace may be used by one stream at a time.  It must be zeroed
  *    once (hylra_workspace_init) before its first use; every call leaves it
- *    ready for the next one.
+ *    ready for the next one of the same batch and head counts, and for the
+ *    paged calls of any shape, which leave it ready for both.  Zero it again
+ *    before dense fp32 calls of another batch or head count.
  */
 #ifndef HYLRA_H_
 #define HYLRA_H_

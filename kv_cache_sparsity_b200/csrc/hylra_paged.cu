@@ -26,9 +26,14 @@ static_assert(sizeof(SelectSmem) + 8 * 2048 * 8 + 16384 * 4 <= kSmemMax &&
               "select kernel shared memory");
 constexpr int kCtasPerSM = 3;        // of the decode kernel, at most
 
+// The status word, the tables' ticket and the partial results.  The dense calls may use
+// the same memory in turn: they need the tickets that follow their status word to be
+// zero, 4 bytes for each 4160 or more of their partials, so in a workspace of `bytes`
+// these end before byte 256 + bytes / 1024, and the partials here begin after it.
 struct PagedLayout {
-  size_t ticket, partials, total;
+  size_t ticket, partial_bytes, total;
   int G;  // CTAs of the decode kernel, at most
+  size_t partials(size_t bytes) const { return (256 + bytes / 1024 + 255) / 256 * 256; }
 };
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -46,8 +51,9 @@ PagedLayout make_layout(int sms) {
   PagedLayout L{};
   L.G = std::min(kCtasPerSM * sms, MAX_GRID);
   L.ticket = 128;
-  L.partials = 256;
-  L.total = L.partials + (size_t)2 * L.G * DecodeShape<128>::SLOT * sizeof(float);
+  L.partial_bytes = (size_t)2 * L.G * DecodeShape<128>::SLOT * sizeof(float);
+  // partials(bytes) + partial_bytes <= bytes from here on: 512 + bytes / 1024 + them
+  L.total = (L.partial_bytes + 512 + (L.partial_bytes + 512) / 1023 + 511) / 256 * 256;
   return L;
 }
 
@@ -232,7 +238,7 @@ int decode(const hylra_paged_t* s, const void* q, const void* K, const void* V,
   p.out = out;
   p.lse = lse;
   p.status = reinterpret_cast<uint32_t*>(w);
-  p.partials = reinterpret_cast<float*>(w + L.partials);
+  p.partials = reinterpret_cast<float*>(w + L.partials(ws_bytes));
   p.B = s->batch;
   p.Hq = s->num_q_heads;
   p.Hkv = s->num_kv_heads;

@@ -858,6 +858,40 @@ def test_one_workspace_serves_every_shape():
             assert torch.equal(o, w[0]) and torch.equal(l, w[1])
 
 
+@pytest.mark.parametrize("batch,hkv,slack", [(40, 8, 0), (3, 2, 0), (40, 8, 5 << 20), (200, 4, 300)])
+def test_one_workspace_serves_dense_and_paged_calls(batch, hkv, slack):
+    """The dense fp32 calls keep state in their workspace; the paged calls leave it as it is."""
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    n = 700
+    q = torch.randn(batch, 4 * hkv, 128, generator=g, device="cuda")
+    kv = torch.randn(2, batch, hkv, n, 128, generator=g, device="cuda")
+    lens = i32([n - b % 5 * 100 for b in range(batch)])
+    shape = H.make_shape(batch, 4 * hkv, hkv, 3, n, dtype=H.FP32, kv_capacity=n)
+    c = T.make_cache((9000, 3, 0, 2000), 64, 8, 2, 128, "bf16", seed=25)
+    r = Requests([5, 0, 40], [3, 100, 2000], 16, seed=6)
+    nbytes = max(H.workspace_bytes(shape), H.paged_workspace_bytes(c.shape)) + slack
+    own = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    both = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+    def dense(ws):
+        out = torch.full((batch, 4 * hkv, 128), math.nan, device="cuda")
+        topk = torch.full((batch, hkv, 3), -9, dtype=torch.int32, device="cuda")
+        H.decode_full(shape, q, kv[0], kv[1], lens, out, topk, ws)
+        return out, topk
+
+    H.workspace_init(own)
+    H.workspace_init(both)
+    want, paged = dense(own), c.decode()
+    c.ws = r.ws = both
+    for _ in range(3):
+        got = c.decode()
+        assert torch.equal(got[0], paged[0]) and torch.equal(got[1], paged[1])
+        r.check()
+        for x, y in zip(dense(both), want):
+            assert torch.equal(x, y)
+    assert c.status() == 0
+
+
 def test_wait_limit_ends_decode_with_a_status():
     """A wait that gives up: the call ends, says so, and leaves the workspace usable."""
     c = T.make_cache((9000, 100), 64, 8, 2, 128, "bf16", seed=24)
