@@ -582,8 +582,9 @@ __global__ void __launch_bounds__(NTHR, 4)
       fence_proxy_async_smem();
     }
     // P and the zeroed rows of all warps.  After a failed wait nothing more is
-    // requested: the others no longer wait for stages, so a copy could land in a stage
-    // still being read.  All warps must agree on it, or a copy would not be waited for.
+    // requested, and all warps agree on it here: a unit is requested by the four of them
+    // or by none, or the bytes of the last requests would not add up and could not be
+    // waited for.
     stop |= __syncthreads_or(*abort_flag);
     // O^T += V^T P^T; the matrix unit's sums cover this unit, the running ones are fp32
     float acc[E::SPLIT][DT][4];
@@ -616,6 +617,10 @@ __global__ void __launch_bounds__(NTHR, 4)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[s]);
     if (i + nst < n && !stop) {
+      // Should this wait be the one that fails, the unit is requested all the same:
+      // the other warps do so too.  The stage's last copies have all arrived, so the
+      // phases hold; its rows may be overwritten under a slower warp, whose outputs
+      // the call's status (HYLRA_STATUS_TIMEOUT) makes void.
       mbar_wait_bounded(&sm.empty[s], ph, abort_flag, p.wait_limit);
       __syncwarp();
       issue(i + nst, s);
