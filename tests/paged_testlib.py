@@ -118,7 +118,7 @@ def attention_tolerance(c: Cache):
     at most (eps/2)^3 = 2^-24 (three bf16 terms) or (eps/2)^2 = 2^-22 (two fp16
     terms).  out = sum p v / sum p doubles the weights' part; the sums have at
     most n additions of 2^-23 each, but run in tiles: at most 8 * 16 in the
-    matrix unit, then one a tile of one CTA, 8 warps at most, and one a CTA that
+    matrix unit, then one a tile of one CTA, 8 for its four warps, and one a CTA that
     holds part of the head: the tiles of 64 tokens or more that one CTA adds up
     and the CTAs are together below n / 128 + 256.  The result is stored in
     fp32 (2^-24), all times the largest |v|.  lse: the same once, plus the
@@ -150,3 +150,68 @@ def check_attention(c: Cache, got, want, what=""):
     err_l = float(np.abs(l[live] - l_ref[live]).max(initial=0.0))
     assert err_o <= tol_o and err_l <= tol_l, (what, err_o, tol_o, err_l, tol_l)
     return err_o, err_l
+
+
+# Inputs whose outputs show the weights themselves: keys and queries along the first dimension
+# (a raw logit is one exact product), values that are unit vectors (token t: dimension t mod d).
+
+FACTORS = (1.0, -1.0, 2.0, 0.5)  # the query of each of four heads
+
+
+def ladder(n, seed=0):
+    """The keys' first elements: multiples of 2^-5 below 8, exact in every type; the first is 0 and
+    the second the largest, so that every head's range of logits is the same for all n >= 2."""
+    c = np.random.default_rng(seed).integers(0, 256, n) / 32
+    c[:2] = (0, 255 / 32)
+    return c
+
+
+def ladder_weights(c, scale):
+    """[heads, n]: the weights relative to the largest, in 64 bits."""
+    a = scale * np.outer(FACTORS, c)
+    return np.exp(a - a.max(1, keepdims=True))
+
+
+def ladder_result(c, w, scale, d):
+    """(out [heads, d], lse [heads]) of these weights."""
+    z = w.sum(1)
+    out = np.stack([np.bincount(np.arange(len(c)) % d, x, d) for x in w]) / z[:, None]
+    return out, scale * np.outer(FACTORS, c).max(1) + np.log(z)
+
+
+def ladder_tolerance(n, d, dtype, scale, heads=1):
+    """(relative, absolute) largest error of an output element, and the largest of an lse.
+
+    A logit less the largest is exact; the scale in base 2 and its product are rounded (2^-24 each), so
+    that exp2's argument is off by X * 2^-23, X its largest size, and a weight by that times ln 2 and
+    by 2^-22 (the exponential).  It goes into the product with V as 16-bit terms: three of bf16 leave
+    2^-24 of it, two of fp16 2^-22 of it or 2^-37 of the largest.  A unit of at most 128 tokens adds to the
+    denominator at most four weights in a lane, then three times over lanes and four over warps (12 of
+    2^-24), and to an output at most two weights of a token's dimension, in the matrix unit (2 of 2^-23),
+    the terms (2 of 2^-24) and the running sum (2^-24).  Dividing is two roundings.
+    More than one unit of 64 tokens or more: a weight is rescaled by the maxima of the units after it in its
+    CTA and then by those of the CTAs, in the join twice.  The arguments of these exponentials add up to X at
+    most; each costs 2^-22 and two roundings; and a sum of one CTA or one of CTAs is rounded per unit.
+    out is a quotient of two such sums.
+    """
+    x = scale * 1.4426950408889634 * max(abs(f) for f in FACTORS) * 255 / 32
+    split = 2.0**-24 if dtype == "bf16" else 2.0**-22
+    weight = math.log(2) * x * 2.0**-23 + 2.0**-22
+    adds = 12 * 2.0**-24
+    unit = 64 if d == 128 else 128
+    if n > unit:
+        units = -(-n // unit)
+        # two CTAs to an SM or more on 148 SMs
+        rescales = -(-units * heads // 296) + 2
+        weight += math.log(2) * x * 2.0**-23 + rescales * (2.0**-22 + 2.0**-23)
+        adds += (units + 16) * 2.0**-24
+    out = 2 * (weight + adds) + split + 2 * 2.0**-23 + 5 * 2.0**-24
+    # an lse: its denominator's error, the logarithm's 2^-22 and the roundings of a sum below this
+    size = x * math.log(2) + math.log(n) + 9
+    return out, (2.0**-37 if dtype == "fp16" else 0.0), weight + adds + size * (2.0**-22 + 4 * 2.0**-24)
+
+
+def ladder_check(got, want, tol):
+    """Whether out and lse are within the tolerance everywhere."""
+    (out, lse), (o, l), (rel, low, abs_l) = got, want, tol
+    return bool(np.all(np.abs(out - o) <= rel * o + low) and np.all(np.abs(lse - l) <= abs_l))

@@ -313,7 +313,7 @@ def test_decode_split_and_join(lens, hq, hkv, d, dtype):
     c = T.make_cache(lens, 128 if d == 128 else 64, hq, hkv, d, dtype, seed=len(lens))
     first = c.decode()
     T.check_attention(c, first, oracle_decode(c))
-    again = c.decode()  # tickets are back at zero, and no order of arrival changes a bit
+    again = c.decode()  # no order of arrival changes a bit
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     assert c.status() == 0
 
@@ -424,6 +424,35 @@ def test_decode_bad_pages_and_lengths():
     c.lens = tuple(lens)
     T.check_attention(c, c.decode(), oracle_decode(c))
     assert c.status() == H.STATUS_BAD_SEQLEN
+
+
+@pytest.mark.parametrize("n", [2, 50, 64, 700, 9000, 40000])
+@pytest.mark.parametrize("d,dtype,page", [(128, "bf16", 64), (128, "fp16", 128), (64, "bf16", 128),
+                                          (64, "fp16", 64), (128, "bf16", 16), (64, "fp16", 16)])
+def test_decode_shows_every_weight(n, d, dtype, page):
+    """Outputs that are sums of at most n / d weights, within a few units in the last place of fp32:
+    weights in fewer 16-bit terms, or a token lost, would show."""
+    c = T.make_cache((n, 3), page, len(T.FACTORS), 1, d, dtype, seed=n)
+    ladders = [T.ladder(k, seed=k) for k in c.lens]
+    c.q.zero_()
+    c.q[:, :, 0] = torch.tensor(T.FACTORS, device="cuda")
+    for b, x in enumerate(ladders):
+        pos = torch.arange(len(x), device="cuda")
+        at = (c.table[b, pos // page].long(), torch.zeros_like(pos), pos % page)
+        rows = torch.zeros(len(x), d, device="cuda", dtype=c.keys.dtype)
+        rows[:, 0] = torch.from_numpy(x).cuda().to(rows.dtype)
+        c.keys[at] = rows
+        c.vals[at] = torch.eye(d, device="cuda", dtype=c.vals.dtype)[pos % d]
+    results = [c.decode()]
+    if c.shape.max_pages <= H.MAX_TOPK:
+        lists = torch.arange(c.shape.max_pages, dtype=torch.int32, device="cuda")
+        results.append(c.decode_topk(lists.expand(2, 1, -1).contiguous()))
+    for out, lse in results:
+        for b, x in enumerate(ladders):
+            want = T.ladder_result(x, T.ladder_weights(x, c.scale), c.scale, d)
+            tol = T.ladder_tolerance(len(x), d, dtype, c.scale, heads=2)
+            assert T.ladder_check((T.f64(out[b]), T.f64(lse[b])), want, tol)
+    assert c.status() == 0
 
 
 def test_decode_without_lse_and_with_shared_pages():

@@ -14,6 +14,8 @@ from kv_cache_sparsity_b200 import build as hbuild
 from kv_cache_sparsity_b200 import hylra as H
 from oracle import paged_oracle as O
 
+import paged_testlib as T
+
 INVALID, UNSUPPORTED = -1, -2
 
 
@@ -310,6 +312,51 @@ def test_type_of_a_shape_refused_by_name(calls, dtype, code):
     with pytest.raises(H.HylraError) as e:
         H.paged_decode(*args)
     assert e.value.code == code and not calls
+
+
+# ------------------------------------------- what the precision tests can see
+
+LADDERS = [(n, d, t) for d in (64, 128) for t in ("bf16", "fp16") for n in (2, 50, 64, 700, 9000, 40000)]
+
+
+def _in_terms(w, dtype, terms):
+    """Weights as the sum of this many 16-bit terms, as the kernel splits them."""
+    t, up = (torch.bfloat16, 1.0) if dtype == "bf16" else (torch.float16, 4096.0)
+    left = torch.from_numpy(w).float() * up
+    total = torch.zeros(w.shape, dtype=torch.float64)
+    for _ in range(terms):
+        part = left.to(t).float()
+        left = left - part
+        total += part.double()
+    return (total / up).numpy()
+
+
+@pytest.mark.parametrize("n,d,dtype", LADDERS)
+def test_precision_tolerance_tells_terms_and_tokens(n, d, dtype):
+    """Weights in the kernel's terms pass; one term, a term less at the sizes of one unit, and a lost
+    token fail.  (Over tens of thousands of tokens the roundings of single fp16 terms average out.)"""
+    scale = 1 / math.sqrt(d)
+    c = T.ladder(n, seed=n)
+    w = T.ladder_weights(c, scale)
+    want = T.ladder_result(c, w, scale, d)
+    tol = T.ladder_tolerance(n, d, dtype, scale)
+
+    def passes(out_weights, z_weights):
+        out, _ = T.ladder_result(c, out_weights, scale, d)
+        _, lse = T.ladder_result(c, z_weights, scale, d)
+        out = out * (out_weights.sum(1) / z_weights.sum(1))[:, None]
+        return T.ladder_check((out, lse), want, tol)
+
+    full = 3 if dtype == "bf16" else 2
+    assert passes(_in_terms(w, dtype, full), w)
+    if 2 < n <= 9000:  # of two weights one is 1
+        assert not passes(_in_terms(w, dtype, 1), w)
+    if n in (50, 64) and dtype == "bf16":
+        assert not passes(_in_terms(w, dtype, 2), w)
+    for lost in sorted({1, n // 2, n - 1}):
+        some = w.copy()
+        some[:, lost] = 0
+        assert not passes(some, some)
 
 
 # ------------------------------------------------------------ oracle pins
