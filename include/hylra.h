@@ -431,7 +431,7 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
  * which outputs over disjoint parts of a sequence can be joined.  A sequence
  * without tokens gets zeros and -inf.  Non-finite q, K or V values that are
  * attended to may make outputs of their own KV head (q: their own head)
- * non-finite, no others.  Results do not depend on the order in which the GPU
+ * non-finite, no others; so may a q.k that no fp32 number holds.  Results do not depend on the order in which the GPU
  * runs the call's parts: equal inputs give equal bits. */
 int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,
                        const void* V_pages, const int32_t* block_table, const int32_t* seqlens,

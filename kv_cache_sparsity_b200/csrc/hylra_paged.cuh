@@ -1366,8 +1366,8 @@ struct AppendParams {
 // before the run come from the pool, or from the input where tokens that were left out
 // part the page's tokens of this call, whose rows in the pool other threads may be
 // writing: the slots are searched back from the run, past any left out, to the first
-// of another page (only where the token before the run may be the page's; 1.3 us, and
-// 0.5 us per 1024 left-out tokens).  Bound by memory: two rows read and two written a
+// of another page (only where the token before the run may be the page's; 1.5 us, and
+// 1 us per 1024 left-out tokens).  Bound by memory: two rows read and two written a
 // token.  63 132 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
 // copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
 // took 127-135 us, two rows in flight per thread do as well as four (eight: 118), and
@@ -1428,15 +1428,18 @@ __global__ void __launch_bounds__(NT_APP)
       len += whole ? 32 : __ffs(out) - 1;
     }
     const bool fills = p.means != nullptr && off + len == ps;
+    // the mean as a sum of shares: 1 / ps is a power of two, so that the roundings are
+    // those of the sum, but it cannot pass fp32 as a sum of bf16 keys can
     float sum[8];
+    const float inv = 1.f / (float)ps;
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = 0.f;
     auto add = [&](const uint4& u) {
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        sum[2 * k] += Elem<T>::value((uint16_t)(w[k] & 0xffffu));
-        sum[2 * k + 1] += Elem<T>::value((uint16_t)(w[k] >> 16));
+        sum[2 * k] = fmaf(Elem<T>::value((uint16_t)(w[k] & 0xffffu)), inv, sum[2 * k]);
+        sum[2 * k + 1] = fmaf(Elem<T>::value((uint16_t)(w[k] >> 16)), inv, sum[2 * k + 1]);
       }
     };
     constexpr int U = 2;  // rows in flight per thread
@@ -1503,8 +1506,8 @@ __global__ void __launch_bounds__(NT_APP)
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[k] = (uint32_t)Elem<T>::bits(sum[2 * k] / (float)ps) |
-               (uint32_t)Elem<T>::bits(sum[2 * k + 1] / (float)ps) << 16;
+        w[k] = (uint32_t)Elem<T>::bits(sum[2 * k]) |
+               (uint32_t)Elem<T>::bits(sum[2 * k + 1]) << 16;
       *reinterpret_cast<uint4*>(p.means + (size_t)(s0 >> psl) * p.Hkv * HD + (size_t)cv * 8) =
           make_uint4(w[0], w[1], w[2], w[3]);
     }

@@ -265,6 +265,29 @@ def test_append_bad_slots_inside_a_page():
     assert check_append(case, 16, slots) == H.STATUS_BAD_INDEX
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_largest_and_smallest_keys(page, dtype):
+    """Means of keys whose sum no fp32 number holds, beside others and alone, and of very small ones."""
+    case = append_case([0, 5], [2 * page, page], page, d=64, dtype=dtype, seed=page)
+    k_new, big = case[4], torch.finfo(T.DTYPES[dtype]).max
+    k_new[:page] = big
+    k_new[2 * page::3] = -big
+    assert check_append(case, page) == 0
+    case = append_case([0, 0], [2 * page, page], page, d=64, dtype=dtype, seed=page)
+    case[4].mul_(2.0 ** (-120 if dtype == "bf16" else -14))
+    shape, keys, vals, means, k_new, v_new, slots = case
+    k, v, m = T.f64(keys), T.f64(vals), T.f64(means)
+    O.append(k, v, m, T.f64(k_new), T.f64(v_new), slots, page)
+    H.paged_append(shape, k_new, v_new, i32(slots), keys, vals, means, T.workspace(shape))
+    # as in check_append, and half a step of the type's subnormal numbers: means of small keys fall
+    # below its smallest normal one (bf16 2^-126, in steps of 2^-133; fp16 2^-14, of 2^-24)
+    tol = np.abs(m) * torch.finfo(means.dtype).eps / 2 + np.nanmax(np.abs(k)) * (page + 1) * 2.0**-24
+    tol = tol + (2.0**-134 if dtype == "bf16" else 2.0**-25)
+    live = ~np.isnan(m)
+    assert np.all(np.abs(T.f64(means) - m)[live] <= tol[live])
+
+
 def test_append_without_means_and_without_tokens():
     shape, keys, vals, means, k_new, v_new, slots = append_case([0], [33], 16)
     ws = T.workspace(shape)
