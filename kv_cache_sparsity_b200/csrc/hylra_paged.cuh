@@ -1344,7 +1344,7 @@ __global__ void __launch_bounds__(NT_SEL, 2)
 constexpr int NT_APP = 256;
 constexpr int COLS_APP = 128;  // 16-byte columns of a CTA
 constexpr int TILE_APP = 64;  // tokens per CTA, at most
-constexpr int BACK_APP = 4 * NT_APP;  // slots of a step of the search behind left-out tokens
+constexpr int BACK_APP = 8 * NT_APP;  // slots of a step of the search behind left-out tokens
 
 struct AppendParams {
   const uint16_t* K_new;
@@ -1366,8 +1366,8 @@ struct AppendParams {
 // before the run come from the pool, or from the input where tokens that were left out
 // part the page's tokens of this call, whose rows in the pool other threads may be
 // writing: the slots are searched back from the run, past any left out, to the first
-// of another page (only where the token before the run may be the page's; 1.5 us, and
-// 1 us per 1024 left-out tokens).  Bound by memory: two rows read and two written a
+// of another page (only where the token before the run may be the page's; 1.3 us, and
+// 0.4 us per 1024 left-out tokens, read 16 bytes at a time).  Bound by memory: two rows read and two written a
 // token.  63 132 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
 // copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
 // took 127-135 us, two rows in flight per thread do as well as four (eight: 118), and
@@ -1470,16 +1470,33 @@ __global__ void __launch_bounds__(NT_APP)
         if (here) from[slot - p0] = u;
         return u <= 0 || slot == p0 || ((uint32_t)slot < (uint32_t)p.num_slots && !here);
       };
-      // first the tokens whose slots are here, then BACK_APP at a time
+      // first the tokens whose slots are here, then BACK_APP at a time, as 16-byte groups
+      // of four (some looked at once more); the one that holds token 0 may begin before it
       static_assert(TILE_APP + MAX_PAGE <= NT_APP, "a thread per slot before the run");
       const int n = l + ps;
       bool end = tid < n && look(t - 1 - tid, tile[l - 1 - (tid < n ? tid : 0)]);
-      for (int u = t - 1 - n - tid; !__syncthreads_or(end); u -= BACK_APP) {
-        int got[BACK_APP / NT_APP];
+      const int skew = (int)((reinterpret_cast<uintptr_t>(p.slots) >> 2) & 3);
+      for (int u = ((t - 1 - n + skew) & ~3) - skew - 4 * tid; !__syncthreads_or(end); u -= BACK_APP) {
+        int4 g[2];
 #pragma unroll
-        for (int v = 0; v < BACK_APP / NT_APP; ++v) got[v] = __ldcg(p.slots + max(u - v * NT_APP, 0));
+        for (int v = 0; v < 2; ++v) {
+          const int at = u - v * (BACK_APP / 2);
+          g[v] = make_int4(-1, -1, -1, -1);
+          if (at >= 0) g[v] = __ldcg(reinterpret_cast<const int4*>(p.slots + at));
+          else if (at > -4) {
+            g[v].w = __ldcg(p.slots + at + 3);
+            if (at > -3) g[v].z = __ldcg(p.slots + at + 2);
+            if (at > -2) g[v].y = __ldcg(p.slots + at + 1);
+          }
+        }
 #pragma unroll
-        for (int v = 0; v < BACK_APP / NT_APP; ++v) end |= look(max(u - v * NT_APP, 0), got[v]);
+        for (int v = 0; v < 2; ++v) {
+          const int at = u - v * (BACK_APP / 2);
+          end |= look(at, g[v].x);
+          end |= look(at + 1, g[v].y);
+          end |= look(at + 2, g[v].z);
+          end |= look(at + 3, g[v].w);
+        }
       }
     }
     for (int i0 = active && keys ? rl : off; i0 < off; i0 += nrow * U) {

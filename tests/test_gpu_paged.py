@@ -258,6 +258,24 @@ def test_append_left_out_tokens_anywhere(tokens, page, hkv):
     assert check_append(with_left_out(case, gaps), page) == 0
 
 
+@pytest.mark.parametrize("skew", [0, 1, 2, 3])
+@pytest.mark.parametrize("gap", [30, 1021, 5000])
+def test_append_slot_maps_at_any_address(skew, gap):
+    """A slot map that begins inside a 16-byte group, searched back to its first token."""
+    shape, keys, vals, means, k_new, v_new, slots = with_left_out(
+        append_case([2, 16, 0, 7], [1, 3, 16, 9], 16, d=64, seed=skew), {0: 5, 1: 2, 10: gap, 21: gap + 1})
+    k, v, m = T.f64(keys), T.f64(vals), T.f64(means)
+    O.append(k, v, m, T.f64(k_new), T.f64(v_new), slots, 16)
+    at = i32([999] * skew + slots + [999])[skew:-1]  # neighbours that are slots of the pool
+    H.paged_append(shape, k_new, v_new, at, keys, vals, means, T.workspace(shape))
+    assert np.array_equal(T.f64(keys), k, equal_nan=True)
+    got, live = T.f64(means), ~np.isnan(m)
+    assert np.array_equal(np.isnan(got), ~live)
+    # as in check_append
+    tol = np.abs(m) * 2.0**-8 + np.nanmax(np.abs(k)) * 17 * 2.0**-24
+    assert np.all(np.abs(got - m)[live] <= tol[live])
+
+
 def test_append_bad_slots_inside_a_page():
     """A slot outside the pool leaves its token out, as -1 does, and says so."""
     case = with_left_out(append_case([0, 2], [40, 30], 16, seed=1), {7: 1, 20: 3, 50: 2})
