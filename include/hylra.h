@@ -56,8 +56,9 @@
  *  * One workspace may be used by one stream at a time.  It must be zeroed
  *    once (hylra_workspace_init) before its first use; every call leaves it
  *    ready for the next one of the same batch and head counts, and for the
- *    paged calls of any shape, which leave it ready for both.  Zero it again
- *    before dense fp32 calls of another batch or head count.
+ *    paged calls of any shape, which leave it ready for both (where every call
+ *    is given the buffer's whole size).  Zero it again before dense fp32 calls
+ *    of another batch or head count.
  */
 #ifndef HYLRA_H_
 #define HYLRA_H_
@@ -431,8 +432,9 @@ int hylra_paged_append(const hylra_paged_t* shape, const void* K_new, const void
  * which outputs over disjoint parts of a sequence can be joined.  A sequence
  * without tokens gets zeros and -inf.  Non-finite q, K or V values that are
  * attended to may make outputs of their own KV head (q: their own head)
- * non-finite, no others; so may a q.k that no fp32 number holds.  Results do not depend on the order in which the GPU
- * runs the call's parts: equal inputs give equal bits. */
+ * non-finite, no others; so may a q.k that no fp32 number holds.  Results do
+ * not depend on the order in which the GPU runs the call's parts: equal inputs
+ * give equal bits. */
 int hylra_paged_decode(const hylra_paged_t* shape, const void* q, const void* K_pages,
                        const void* V_pages, const int32_t* block_table, const int32_t* seqlens,
                        float* out, float* lse, void* workspace, size_t workspace_bytes,

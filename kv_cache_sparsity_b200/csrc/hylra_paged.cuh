@@ -1368,9 +1368,9 @@ struct AppendParams {
 // part the page's tokens of this call, whose rows in the pool other threads may be
 // writing: the slots are searched back from the run, past any left out, to the first
 // of another page (only where the token before the run may be the page's; 1.3 us, and
-// 0.4 us per 1024 left-out tokens, read 16 bytes at a time).  Bound by memory: two rows read and two written a
-// token.  63 132 tokens of 8 heads, d 128: 103 us, of which the means take 2; a plain
-// copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
+// 0.4 us per 1024 left-out tokens, read 16 bytes at a time).
+// Bound by memory: two rows read and two written a token.  63 132 tokens of 8 heads,
+// d 128: 103 us, of which the means take 2; a plain copy of as many bytes takes 83.  Reading a filled page's rows once more for its mean
 // took 127-135 us, two rows in flight per thread do as well as four (eight: 118), and
 // 64 columns a CTA lose a fifth with 16-token pages.
 template <int HD, typename T>
@@ -1461,7 +1461,8 @@ __global__ void __launch_bounds__(NT_APP)
     // rows before the run: from the pool, or from this call, of which the token
     // before the run is then another or was left out
     const int p0 = s0 - off;  // the page's first slot
-    const bool mixed = off > 0 && t > 0 && (tile[l - 1] < 0 || (tile[l - 1] >= p0 && tile[l - 1] < s0));
+    const bool mixed =
+        off > 0 && t > 0 && (tile[l - 1] < 0 || (tile[l - 1] >= p0 && tile[l - 1] < s0));
     if (mixed) {
       for (int i = tid; i < off; i += NT_APP) from[i] = -1;
       __syncthreads();
@@ -1477,7 +1478,8 @@ __global__ void __launch_bounds__(NT_APP)
       const int n = l + ps;
       bool end = tid < n && look(t - 1 - tid, tile[l - 1 - (tid < n ? tid : 0)]);
       const int skew = (int)((reinterpret_cast<uintptr_t>(p.slots) >> 2) & 3);
-      for (int u = ((t - 1 - n + skew) & ~3) - skew - 4 * tid; !__syncthreads_or(end); u -= BACK_APP) {
+      const int top = ((t - 1 - n + skew) & ~3) - skew;  // the group of the last slot not seen
+      for (int u = top - 4 * tid; !__syncthreads_or(end); u -= BACK_APP) {
         int4 g[2];
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
